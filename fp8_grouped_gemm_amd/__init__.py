@@ -369,3 +369,20 @@ class MoEForward:
             self.close()
         except Exception:
             pass
+
+
+# --- row operators (include/moe_ops.h) -------------------------------------
+
+def __getattr__(name):
+    # loaded on first use: the operators need torch, this module does not
+    if name == "ops" or name in _OPS_NAMES:
+        import importlib
+        ops = importlib.import_module(".ops", __name__)
+        globals().update({n: getattr(ops, n) for n in _OPS_NAMES})
+        return ops if name == "ops" else getattr(ops, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+_OPS_NAMES = ("moe_permute", "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd",
+              "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4",
+              "MOE_DTYPE_BF16", "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_U8")

@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_fp8.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["moe_api.cpp", "route.hip", "gemm_direct.hip", "gemm_lds.hip", "gemm_lds160.hip", "gemm_sa.hip",
-           "gemm_mx.hip", "pack.hip", "quant.hip"]
+           "gemm_mx.hip", "pack.hip", "quant.hip", "ops_api.cpp", "rows.hip", "mxfp4.hip",
+           "gemm_mxfp4.hip"]
 PEAKS_LIB = os.path.join(HERE, "libmoe_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]
 

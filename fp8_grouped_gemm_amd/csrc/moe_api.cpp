@@ -13,6 +13,7 @@
 
 #include "../../include/moe_fp8.h"
 #include "moe_internal.h"
+#include "ops_internal.h"
 
 struct moe_plan {
     moe_shape_t shape;
@@ -545,6 +546,12 @@ moe::RouteArgs route_args(const moe_shape_t& s, int T, const Layout& L, void* ws
 }
 
 }  // namespace
+
+namespace moe {
+
+int device_status() { return device_ok(); }
+
+}  // namespace moe
 
 extern "C" {
 

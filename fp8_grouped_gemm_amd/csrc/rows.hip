@@ -1,0 +1,274 @@
+// Token rows into expert order and back (include/moe_ops.h: moe_permute,
+// moe_permute_bwd, moe_unpermute, moe_unpermute_bwd), over the lists of the
+// routing planner: src_row[f] the pool row of slot f = t*K + j, row_src[r] the
+// slot of pool row r.
+//   permute        xp[src_row[f]] = x[f / K]
+//   its gradient   dx[t] = sum_j dxp[src_row[tK + j]]
+//   unpermute      y[t] = sum_j w[tK + j] yp[src_row[tK + j]]
+//   its gradients  dyp[src_row[f]] = w[f] dy[f / K],  dw[f] = dy[f / K] . yp[src_row[f]]
+//
+// All four move bytes and compute next to nothing, so HBM bounds them.  They
+// walk the token side, not the pool: a token's row is read once (or its
+// sums stay in registers) and its K pool rows are written or read whole,
+// where walking the pool would read every token row K times.  Nothing is
+// summed by atomics: a token's sum runs over its slots in ascending j.
+//
+// Every list entry is range-checked before it forms an address.
+#include "../../include/moe_ops.h"
+#include "ops_internal.h"
+#include "rows_device.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPadRows = 4;  // pool rows each wave looks over for padding
+
+// Zeros the padding rows (row_src outside [0, TK)) among pool rows
+// [r0, r0 + kPadRows) below `used`, by one wave.
+__device__ __forceinline__ void clear_padding(const RowsArgs& a, int r0, int row_bytes, int lane)
+{
+    const int used = a.used ? min(*a.used, a.R) : a.R;
+    const int end = min(r0 + kPadRows, used);
+    const rows_u32x4 zero = {0, 0, 0, 0};
+    for (int r = r0; r < end; ++r) {
+        const int f = a.row_src[r];
+        if (f >= 0 && f < a.T * a.K)
+            continue;
+        char* p = a.pool_out + (int64_t)r * a.pool_out_ld;
+        int at = lane * 16;
+        for (; at + 16 <= row_bytes; at += 64 * 16)
+            store16(p + at, zero);
+        for (; at < row_bytes; ++at)  // the one lane (if any) holding the ragged end
+            p[at] = 0;
+    }
+}
+
+// Workgroups of one launch: token_wgs over tokens, then those that look for
+// padding.
+unsigned pad_wgs(const RowsArgs& a)
+{
+    const int per_wg = kPadRows * kThreads / 64;
+    return a.row_src ? (unsigned)((a.R + per_wg - 1) / per_wg) : 0u;
+}
+
+// Threads along a row: the smallest power of two that covers its n vectors,
+// 16 to 256 (narrow rows share a workgroup).
+int row_threads(int64_t n)
+{
+    int t = 16;
+    while (t < kThreads && t < n)
+        t *= 2;
+    return t;
+}
+
+}  // namespace
+
+// x row -> its K pool rows, one 16-byte piece per thread.  A row's last piece
+// reaches back to stay whole (it writes bytes the previous piece also
+// writes, with the same values); rows under 16 bytes go byte by byte.
+__global__ __launch_bounds__(kThreads) void permute_rows(RowsArgs a, int row_bytes, int tpr,
+                                                         int pieces, unsigned token_wgs)
+{
+    if (blockIdx.x >= token_wgs) {
+        const int wave = (blockIdx.x - token_wgs) * (kThreads / 64) + (threadIdx.x >> 6);
+        clear_padding(a, wave * kPadRows, row_bytes, threadIdx.x & 63);
+        return;
+    }
+    const unsigned g = blockIdx.x / pieces;
+    const int t = g * (kThreads / tpr) + threadIdx.x / tpr;
+    int at = ((blockIdx.x - g * pieces) * tpr + threadIdx.x % tpr) * 16;
+    if (t >= a.T || at >= row_bytes)
+        return;
+    const char* src = a.tok + (int64_t)t * a.tok_ld;
+    const int32_t* slot = a.src_row + (int64_t)t * a.K;
+    if (row_bytes < 16) {
+        for (int j = 0; j < a.K; ++j) {
+            const int r = slot[j];
+            if (r >= 0 && r < a.R)
+                for (int i = 0; i < row_bytes; ++i)
+                    a.pool_out[(int64_t)r * a.pool_out_ld + i] = src[i];
+        }
+        return;
+    }
+    at = min(at, row_bytes - 16);
+    const rows_u32x4 v = load16(src + at);
+    for (int j = 0; j < a.K; ++j) {
+        const int r = slot[j];
+        if (r >= 0 && r < a.R)
+            store16(a.pool_out + (int64_t)r * a.pool_out_ld + at, v);
+    }
+}
+
+// out[t] = sum_j w[tK + j] pool[src_row[tK + j]], j ascending, one vector of the row
+// per thread; four slots' loads are in flight at a time.
+template <class E, bool W>
+__global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int pieces)
+{
+    const unsigned g = blockIdx.x / pieces;
+    const int t = g * (kThreads / tpr) + threadIdx.x / tpr;
+    const int c = ((blockIdx.x - g * pieces) * tpr + threadIdx.x % tpr) * E::VEC;
+    if (t >= a.T || c >= a.width)
+        return;
+    const int n = a.width - c;
+    const int32_t* slot = a.src_row + (int64_t)t * a.K;
+    const float* w = W ? a.w + (int64_t)t * a.K : nullptr;
+    float acc[E::VEC];
+#pragma unroll
+    for (int i = 0; i < E::VEC; ++i)
+        acc[i] = 0.f;
+    constexpr int U = 4;
+    for (int j0 = 0; j0 < a.K; j0 += U) {
+        float v[U][E::VEC], wt[U];
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = j0 + u < a.K ? slot[j0 + u] : -1;
+            on[u] = r >= 0 && r < a.R;
+            wt[u] = 1.f;
+            if (on[u]) {
+                if (W)
+                    wt[u] = w[j0 + u];
+                load_vec<E>(a.pool + (int64_t)r * a.pool_ld + (int64_t)c * E::SIZE, n, v[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (on[u])
+#pragma unroll
+                for (int i = 0; i < E::VEC; ++i)
+                    acc[i] = W ? __builtin_fmaf(wt[u], v[u][i], acc[i]) : acc[i] + v[u][i];
+    }
+    store_vec<E>(a.tok_out + (int64_t)t * a.tok_ld + (int64_t)c * E::SIZE, n, acc);
+}
+
+// dyp row and dw of one slot per wave: the lanes stride over the row, write
+// w dy and sum dy yp, and the wave's 64 sums meet in a butterfly (a fixed
+// order).  Consecutive waves take consecutive slots, so the K waves of a
+// token read its dy row together.
+template <class E, bool DYP, bool DW>
+__global__ __launch_bounds__(kThreads) void unpermute_grad(RowsArgs a, unsigned token_wgs)
+{
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blockIdx.x >= token_wgs) {
+        clear_padding(a, ((blockIdx.x - token_wgs) * (kThreads / 64) + wave) * kPadRows,
+                      a.width * E::SIZE, lane);
+        return;
+    }
+    const int f = blockIdx.x * (kThreads / 64) + wave;
+    if (f >= a.T * a.K)
+        return;
+    const int r = a.src_row[f];
+    if (r < 0 || r >= a.R) {
+        if (DW && lane == 0)
+            a.dw[f] = 0.f;
+        return;
+    }
+    const char* dy = a.tok + (int64_t)(f / a.K) * a.tok_ld;
+    const char* yp = DW ? a.pool + (int64_t)r * a.pool_ld : nullptr;
+    char* dyp = DYP ? a.pool_out + (int64_t)r * a.pool_out_ld : nullptr;
+    const float w = a.w ? a.w[f] : 1.f;
+    float sum = 0.f;
+#pragma unroll 2
+    for (int c = lane * E::VEC; c < a.width; c += 64 * E::VEC) {
+        const int n = a.width - c;
+        float d[E::VEC], y[E::VEC];
+        load_vec<E>(dy + (int64_t)c * E::SIZE, n, d);
+        if (DW) {
+            load_vec<E>(yp + (int64_t)c * E::SIZE, n, y);
+#pragma unroll
+            for (int i = 0; i < E::VEC; ++i)
+                sum = __builtin_fmaf(d[i], y[i], sum);
+        }
+        if (DYP) {
+#pragma unroll
+            for (int i = 0; i < E::VEC; ++i)
+                d[i] *= w;
+            store_vec<E>(dyp + (int64_t)c * E::SIZE, n, d);
+        }
+    }
+    if (DW) {
+#pragma unroll
+        for (int x = 32; x >= 1; x >>= 1)
+            sum += __shfl_xor(sum, x);
+        if (lane == 0)
+            a.dw[f] = sum;
+    }
+}
+
+// ------------------------------------------------------------ launchers
+
+hipError_t launch_permute(const RowsArgs& a, hipStream_t s)
+{
+    const int size = a.dtype == MOE_DTYPE_F32 ? 4 : a.dtype == MOE_DTYPE_U8 ? 1 : 2;
+    const int row_bytes = a.width * size;
+    const int64_t n = (row_bytes + 15) / 16;
+    const int tpr = row_threads(n), per = kThreads / tpr;
+    const int pieces = (int)((n + tpr - 1) / tpr);
+    const int64_t wgs = (int64_t)((a.T + per - 1) / per) * pieces;
+    const unsigned pad = pad_wgs(a);
+    if (wgs + pad >= (INT64_C(1) << 31))
+        return hipErrorInvalidValue;
+    if (wgs + pad == 0)
+        return hipSuccess;
+    hipLaunchKernelGGL(permute_rows, dim3((unsigned)wgs + pad), dim3(kThreads), 0, s, a, row_bytes,
+                       tpr, pieces, (unsigned)wgs);
+    return hipGetLastError();
+}
+
+template <class E>
+static hipError_t launch_token_sums(const RowsArgs& a, hipStream_t s)
+{
+    const int64_t n = (a.width + E::VEC - 1) / E::VEC;
+    const int tpr = row_threads(n), per = kThreads / tpr;
+    const int pieces = (int)((n + tpr - 1) / tpr);
+    const int64_t wgs = (int64_t)((a.T + per - 1) / per) * pieces;
+    if (wgs >= (INT64_C(1) << 31))
+        return hipErrorInvalidValue;
+    if (a.w)
+        hipLaunchKernelGGL((token_sums<E, true>), dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
+    else
+        hipLaunchKernelGGL((token_sums<E, false>), dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
+    return hipGetLastError();
+}
+
+hipError_t launch_unpermute(const RowsArgs& a, hipStream_t s)
+{
+    switch (a.dtype) {
+    case MOE_DTYPE_BF16: return launch_token_sums<Bf16>(a, s);
+    case MOE_DTYPE_F16: return launch_token_sums<F16>(a, s);
+    case MOE_DTYPE_F32: return launch_token_sums<F32>(a, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+template <class E>
+static hipError_t launch_grad(const RowsArgs& a, hipStream_t s)
+{
+    const unsigned wgs = (unsigned)(((int64_t)a.T * a.K + kThreads / 64 - 1) / (kThreads / 64));
+    const unsigned pad = a.pool_out ? pad_wgs(a) : 0u;
+    const dim3 grid(wgs + pad), block(kThreads);
+    if (wgs + pad == 0)
+        return hipSuccess;
+    if (a.pool_out && a.dw)
+        hipLaunchKernelGGL((unpermute_grad<E, true, true>), grid, block, 0, s, a, wgs);
+    else if (a.pool_out)
+        hipLaunchKernelGGL((unpermute_grad<E, true, false>), grid, block, 0, s, a, wgs);
+    else
+        hipLaunchKernelGGL((unpermute_grad<E, false, true>), grid, block, 0, s, a, wgs);
+    return hipGetLastError();
+}
+
+hipError_t launch_unpermute_bwd(const RowsArgs& a, hipStream_t s)
+{
+    switch (a.dtype) {
+    case MOE_DTYPE_BF16: return launch_grad<Bf16>(a, s);
+    case MOE_DTYPE_F16: return launch_grad<F16>(a, s);
+    case MOE_DTYPE_F32: return launch_grad<F32>(a, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace moe
