@@ -258,31 +258,76 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
 // ---------------------------------------------------------------- tiles
 //
 // BM x BN tile per workgroup of WM x WN waves, each MI x NI subtiles of
-// 32 x 32; K in stages of 256 (128 bytes of each row), staged in LDS by
-// asynchronous copies into one of two buffers while the other is multiplied.
-// One copy instruction of a wave brings 8 rows x 128 bytes -- whole lines
-// from memory, 1 KiB in a row of LDS -- and a row's eight 16-byte chunks sit
-// in LDS at position chunk ^ key(row), key = (row & 7) ^ (row >> 3 & 1): any 8
-// (16) consecutive rows then hold a given chunk in different banks, so the
-// fragment reads run without conflicts.  Scales pass through registers: each
-// thread loads the 8 codes of a row one stage ahead and leaves them in LDS,
-// and one byte permute of a row's 8 codes gives the MFMA's scale register
-// for all four 64-wide K steps of the stage (lane group g takes the codes
-// 2s + g).  Blocks past the end of K are copied from 16 zero bytes, scale 1.
-__device__ __constant__ const uint4 kZeroBlock = {0, 0, 0, 0};
+// 32 x 32; K in stages of 256 (one 128-byte line of each row, four MFMA
+// steps), copied asynchronously into a ring of NBUF LDS buffers.
+//
+// Pipeline: a wave reads the fragments of step s + 1 while it multiplies
+// step s, and the stage's one barrier stands before its last products, so the
+// matrix cores run through it.  At the barrier every wave has read its last
+// fragments of the stage, whose buffer is then free, and its copies of the
+// next stage have landed; the copies into the freed buffer go out right
+// behind it, one by one between products (issued together they fill the
+// memory pipeline and hold the products back).
+//
+// One copy instruction of a wave brings 8 rows x 128 bytes, whole lines from
+// memory and 1 KiB in a row of LDS (16 rows x 64 bytes took 1.6 times as
+// long per byte from L2).  A row's eight 16-byte chunks sit at position
+// chunk ^ key(row), key = (row & 7) ^ (row >> 3 & 1): any 8 (16) consecutive
+// rows then hold a given chunk in different banks of 32 (64), and the
+// fragment reads run without conflicts.  Blocks past the end of K are copied
+// from outside the buffer resource, which reads as zeros.
+//
+// Scale codes pass through registers into LDS, 32 (4 stages) of a row at a
+// time; a byte permute of a row's 8 codes of one stage gives the MFMAs' scale
+// register for its four steps (lane group g takes codes 2 s + g, step s byte
+// s).  Codes past the end of K are 127, scale 1.
+typedef int v4i __attribute__((ext_vector_type(4)));
+constexpr int kCodeStages = 4;  // stages per load of scale codes
 
-template <class T, int WM, int WN, int MI, int NI>
+template <class T, int WM, int WN, int MI, int NI, int NBUF>
+struct TileCfg {
+    static constexpr int BM = WM * MI * 32, BN = WN * NI * 32, ROWS = BM + BN;
+    static constexpr int W = WM * WN, TH = 64 * W;
+    static constexpr int STAGE = ROWS * 128;
+    static constexpr int COPIES = ROWS / 8 / W;         // per wave and stage
+    static constexpr int CODES = (ROWS + TH - 1) / TH;  // rows of scale codes per thread
+    static constexpr int SC = kCodeStages * ROWS * 8;   // one load of codes in LDS
+    static constexpr int SMEM = NBUF * STAGE + 2 * SC;
+    // the result leaves through LDS, 32 rows of a wave at a time
+    static constexpr int OUT_LD = NI * 32 * T::SIZE + 16;
+    static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0, "whole copies per wave and operand");
+    static_assert(W % 2 == 0, "a wave's copies share the parity of row / 8");
+    static_assert(SMEM <= 160 * 1024 && W * 32 * OUT_LD <= SMEM, "LDS");
+};
+
+// A buffer resource of `bytes` bytes at p (both wave-uniform); what lies past
+// them reads as zeros.
+__device__ __forceinline__ v4i byte_rsrc(const uint8_t* p, uint32_t bytes)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    v4i r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32) & 0xFFFF);
+    r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
+    r[3] = 0x00020000;
+    return r;
+}
+
+// 16 bytes per lane from byte `off` of the resource to LDS at lds + 16 * lane.
+__device__ __forceinline__ void dma16_rsrc(const v4i& r, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r),
+                 "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory", "m0");
+}
+
+template <class T, int WM, int WN, int MI, int NI, int NBUF>
 __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col_tiles)
 {
-    constexpr int BM = WM * MI * 32, BN = WN * NI * 32;
-    constexpr int W = WM * WN, TH = 64 * W;
-    constexpr int ROWS = BM + BN;              // of both operands, a's first
-    constexpr int STAGE = ROWS * 128;
-    constexpr int COPIES = ROWS / 8 / W;       // per wave and stage
-    constexpr int SCALES = (ROWS + TH - 1) / TH;
-    static_assert(ROWS % (8 * W) == 0, "whole copies per wave");
+    using C = TileCfg<T, WM, WN, MI, NI, NBUF>;
+    constexpr int BM = C::BM, BN = C::BN, ROWS = C::ROWS, W = C::W, TH = C::TH;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-    uint8_t* const sc = smem + 2 * STAGE;      // [2][ROWS][8]
+    uint8_t* const sc = smem + NBUF * C::STAGE;  // [2][kCodeStages][ROWS][8]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int ct = 0;
@@ -291,77 +336,75 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
         return;
     const int col0 = ct * BN, cols = min(BN, a.N - col0);
     const int nb = a.K / 32, stages = (nb + 7) / 8;
-    const uint8_t* const abase = a.a + (int64_t)t.row0 * (a.K / 2);
-    const uint8_t* const bbase = a.b + ((int64_t)t.e * a.N + col0) * (a.K / 2);
+    const uint32_t pitch = a.K / 2;
+    const v4i ra = byte_rsrc(a.a + (int64_t)t.row0 * pitch, t.rows * pitch);
+    const v4i rb = byte_rsrc(a.b + ((int64_t)t.e * a.N + col0) * pitch, cols * pitch);
     const uint8_t* const asf = a.a_sf + (int64_t)t.row0 * nb;
     const uint8_t* const bsf = a.b_sf + ((int64_t)t.e * a.N + col0) * nb;
 
-    // Copies: instruction q of this wave brings LDS rows 8 (q W + wave) ..
-    // + 7, lane l the chunk at position l % 8 of row l / 8.
-    uint32_t off[COPIES];
+    // Copy q of this wave brings LDS rows 8 (q W + wave) .. + 7, lane l the
+    // chunk at position l % 8 of row l / 8; rows past the tile lie outside the
+    // resource (zeros).  off0: the lane's place in stage 0 of copy 0.
+    const int chunk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+    const uint32_t off0 = (8 * wave + (lane >> 3)) * pitch + chunk * 16;
+    const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+    auto copy = [&](int st, int buf, int q) {
+        constexpr int QA = BM / 8 / W;  // copies of a's rows
+        const uint32_t at = off0 + (q < QA ? q : q - QA) * (8 * W) * pitch + st * 128;
+        dma16_rsrc(q < QA ? ra : rb, st * 8 + chunk < nb ? at : 0x80000000u,
+                   lds0 + buf * C::STAGE + q * W * 1024);
+    };
+    // Scale codes: thread i takes rows i, i + TH, ... of the ROWS.
+    auto code_row = [&](int row) {  // rows past the tile repeat its last
+        return row < BM ? asf + min(row, t.rows - 1) * nb : bsf + min(row - BM, cols - 1) * nb;
+    };
+    uint32_t codes[C::CODES][2 * kCodeStages];
+    auto fetch_codes = [&](int g) {
+        struct __attribute__((packed, aligned(1))) U4 { uint32_t v[4]; };
 #pragma unroll
-    for (int q = 0; q < COPIES; ++q) {
-        const int r8 = q * W + wave;
-        const int row = 8 * r8 + (lane >> 3);
-        const int key = ((lane >> 3) ^ (r8 & 1)) & 7;
-        const int c = (lane & 7) ^ key;
-        const int live = row < BM ? min(row, t.rows - 1) : min(row - BM, cols - 1);
-        off[q] = (uint32_t)live * (uint32_t)(a.K / 2) + c * 16;
-    }
-    const uint32_t lds0 = lds_addr(smem);
-    auto copy = [&](int stage, int buf) {
-        const bool ragged = stage * 8 + 8 > nb;
+        for (int q = 0; q < C::CODES; ++q) {
+            const int row = q * TH + threadIdx.x;
+            const uint8_t* p = code_row(row) + g * 8 * kCodeStages;
+            if ((g + 1) * 8 * kCodeStages <= nb) {
 #pragma unroll
-        for (int q = 0; q < COPIES; ++q) {
-            const int r8 = q * W + wave;
-            const uint8_t* base = (8 * r8 < BM ? abase : bbase) + (int64_t)stage * 128;
-            const uint32_t dst = lds0 + buf * STAGE + r8 * 1024;
-            if (!ragged) {
-                dma16_off(base, off[q], dst);
-            } else {
-                const int c = (lane & 7) ^ (((lane >> 3) ^ (r8 & 1)) & 7);
-                const void* src = stage * 8 + c < nb ? (const void*)(base + off[q]) : (const void*)&kZeroBlock;
-                dma16(src, dst);
+                for (int i = 0; i < kCodeStages / 2; ++i) {
+                    const U4 u = *reinterpret_cast<const U4*>(p + 16 * i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        codes[q][4 * i + j] = u.v[j];
+                }
+            } else {  // the group K ends in, byte by byte
+                const int last = nb - 1 - g * 8 * kCodeStages;
+#pragma unroll
+                for (int i = 0; i < 2 * kCodeStages; ++i) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t c = p[max(0, min(4 * i + j, last))];
+                        w |= (4 * i + j <= last ? c : 127u) << (8 * j);
+                    }
+                    codes[q][i] = w;
+                }
             }
         }
     };
-    // Scales: thread i takes row i (and i + TH ...) of the ROWS.
-    uint2 codes[SCALES];
-    auto fetch_scales = [&](int stage) {
+    auto leave_codes = [&](int g) {
 #pragma unroll
-        for (int q = 0; q < SCALES; ++q) {
+        for (int q = 0; q < C::CODES; ++q) {
             const int row = q * TH + threadIdx.x;
-            codes[q] = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            if (row >= ROWS)
-                continue;
-            const uint8_t* p = (row < BM ? asf + (int64_t)min(row, t.rows - 1) * nb
-                                         : bsf + (int64_t)min(row - BM, cols - 1) * nb) + stage * 8;
-            if (stage * 8 + 8 <= nb) {
-                struct __attribute__((packed, aligned(1))) U2 { uint32_t x, y; };
-                const U2 u = *reinterpret_cast<const U2*>(p);
-                codes[q] = make_uint2(u.x, u.y);
-            } else {
-                uint32_t w[2] = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+            if (ROWS % TH == 0 || row < ROWS)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (stage * 8 + i < nb)
-                        w[i / 4] = (w[i / 4] & ~(0xFFu << (8 * (i % 4)))) | ((uint32_t)p[i] << (8 * (i % 4)));
-                codes[q] = make_uint2(w[0], w[1]);
-            }
-        }
-    };
-    auto leave_scales = [&](int buf) {
-#pragma unroll
-        for (int q = 0; q < SCALES; ++q) {
-            const int row = q * TH + threadIdx.x;
-            if (row < ROWS)
-                *reinterpret_cast<uint2*>(sc + (buf * ROWS + row) * 8) = codes[q];
+                for (int i = 0; i < kCodeStages; ++i)
+                    *reinterpret_cast<uint2*>(sc + (g & 1) * C::SC + (i * ROWS + row) * 8) =
+                        make_uint2(codes[q][2 * i], codes[q][2 * i + 1]);
         }
     };
 
     const int wm = wave / WN, wn = wave % WN;
     const int lr = lane & 31, lg = lane >> 5;
     const int key = (lr & 7) ^ ((lr >> 3) & 1);
+    const uint32_t la = (wm * MI * 32 + lr) * 128, lb = (BM + wn * NI * 32 + lr) * 128;
+    const uint32_t ca = (wm * MI * 32 + lr) * 8, cb = (BM + wn * NI * 32 + lr) * 8;
     const uint32_t pick = lg ? 0x07050301u : 0x06040200u;  // codes 1,3,5,7 or 0,2,4,6
     v16f acc[MI][NI];
 #pragma unroll
@@ -371,73 +414,145 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 acc[m][n][i] = 0.f;
-
-    fetch_scales(0);
-    copy(0, 0);
-    leave_scales(0);
-    MOE_WAIT_VMCNT(0);
-    __syncthreads();
-    for (int st = 0; st < stages; ++st) {
-        const int buf = st & 1;
-        if (st + 1 < stages) {
-            fetch_scales(st + 1);
-            copy(st + 1, buf ^ 1);
-        }
-        const uint8_t* const la = smem + buf * STAGE + (wm * MI * 32 + lr) * 128;
-        const uint8_t* const lb = smem + buf * STAGE + (BM + wn * NI * 32 + lr) * 128;
-        const uint8_t* const sa0 = sc + (buf * ROWS + wm * MI * 32 + lr) * 8;
-        const uint8_t* const sb0 = sc + (buf * ROWS + BM + wn * NI * 32 + lr) * 8;
-        int sa[MI], sb[NI];
+    uint4 fa[2][MI], fb[2][NI];  // fragments of even and odd steps
+    uint2 ua[MI], ub[NI];        // codes of the next stage as read
+    int sa[MI], sb[NI];          // scale registers of the current one
+    auto read = [&](int buf, int s) {
+        const uint8_t* const p = smem + buf * C::STAGE + (((2 * s + lg) ^ key) * 16);
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+            fa[s & 1][m] = *reinterpret_cast<const uint4*>(p + la + m * 4096);
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            fb[s & 1][n] = *reinterpret_cast<const uint4*>(p + lb + n * 4096);
+    };
+    auto read_codes = [&](int st) {
+        const uint8_t* const p = sc + ((st / kCodeStages) & 1) * C::SC + (st % kCodeStages) * ROWS * 8;
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+            ua[m] = *reinterpret_cast<const uint2*>(p + ca + m * 256);
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            ub[n] = *reinterpret_cast<const uint2*>(p + cb + n * 256);
+    };
+    // step S's products; `between(m)` runs after those of row subtile m
+    auto mul = [&](auto S, auto between) {
+        constexpr int s = decltype(S)::value;
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
-            const uint2 u = *reinterpret_cast<const uint2*>(sa0 + m * 256);
-            sa[m] = (int)__builtin_amdgcn_perm(u.y, u.x, pick);
-        }
-#pragma unroll
-        for (int n = 0; n < NI; ++n) {
-            const uint2 u = *reinterpret_cast<const uint2*>(sb0 + n * 256);
-            sb[n] = (int)__builtin_amdgcn_perm(u.y, u.x, pick);
-        }
-        auto step = [&](auto S) {
-            constexpr int s = decltype(S)::value;
-            const int at = ((2 * s + lg) ^ key) * 16;
-            uint4 fa[MI], fb[NI];
-#pragma unroll
-            for (int m = 0; m < MI; ++m)
-                fa[m] = *reinterpret_cast<const uint4*>(la + m * 4096 + at);
 #pragma unroll
             for (int n = 0; n < NI; ++n)
-                fb[n] = *reinterpret_cast<const uint4*>(lb + n * 4096 + at);
+                acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    e2m1_operand(fa[s & 1][m]), e2m1_operand(fb[s & 1][n]), acc[m][n], 4, 4, s, sa[m], s, sb[n]);
+            __builtin_amdgcn_sched_barrier(0);
+            between(m);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto nothing = [](int) {};
+    constexpr int HALF = C::COPIES / 2;
+
+    // prologue: the first codes, stages 0 .. NBUF - 2 and half of the next
+    fetch_codes(0);
+    leave_codes(0);
 #pragma unroll
-            for (int m = 0; m < MI; ++m)
+    for (int st = 0; st < NBUF - 1; ++st)
 #pragma unroll
-                for (int n = 0; n < NI; ++n)
-                    acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        e2m1_operand(fa[m]), e2m1_operand(fb[n]), acc[m][n], 4, 4, s, sa[m], s, sb[n]);
-        };
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 3>{});
-        if (st + 1 < stages)
-            leave_scales(buf ^ 1);
-        // the next stage's copies have landed, and no wave still reads this one
-        MOE_WAIT_VMCNT(0);
+        for (int q = 0; q < C::COPIES; ++q)
+            copy(st, st, q);
+    MOE_WAIT_VMCNT((NBUF - 2) * C::COPIES);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < HALF; ++q)
+        copy(NBUF - 1, NBUF - 1, q);
+    read(0, 0);
+    read_codes(0);
+    int buf = 0;  // of the current stage
+    // One stage, as one basic block: past a branch the compiler sinks
+    // products to where their sums are used.  (So the copies of stages past
+    // the last are issued too, and read zeros without a memory access.)
+    auto stage = [&](int st, auto LAST) {
+        constexpr bool last = decltype(LAST)::value;  // of its code group
+        const int next = buf + 1 == NBUF ? 0 : buf + 1, prev = buf == 0 ? NBUF - 1 : buf - 1;
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+            sa[m] = (int)__builtin_amdgcn_perm(ua[m].y, ua[m].x, pick);
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            sb[n] = (int)__builtin_amdgcn_perm(ub[n].y, ub[n].x, pick);
+        read(buf, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        mul(std::integral_constant<int, 0>{}, [&](int m) {
+#pragma unroll
+            for (int q = HALF + m; q < C::COPIES; q += MI)
+                copy(st + NBUF - 1, prev, q);
+        });
+        read(buf, 2);
+        __builtin_amdgcn_sched_barrier(0);
+        mul(std::integral_constant<int, 1>{}, nothing);
+        read(buf, 3);
+        __builtin_amdgcn_sched_barrier(0);
+        mul(std::integral_constant<int, 2>{}, nothing);
+        // stage st + 1 landed, NBUF - 2 newer ones may be in flight (the
+        // compiler's wait for the code loads takes in those too)
+        if constexpr (last)
+            leave_codes(st / kCodeStages + 1);
+        MOE_WAIT_VMCNT((NBUF - 2) * C::COPIES);
         __syncthreads();
+        read(next, 0);  // (past the last stage: read, not used)
+        read_codes(st + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        mul(std::integral_constant<int, 3>{}, [&](int m) {
+#pragma unroll
+            for (int q = m; q < HALF; q += MI)
+                copy(st + NBUF, buf, q);
+        });
+        buf = next;
+    };
+    for (int g = 0; g * kCodeStages < stages; ++g) {
+        if ((g + 1) * kCodeStages < stages)
+            fetch_codes(g + 1);
+        const int end = min(stages, (g + 1) * kCodeStages);
+        for (int st = g * kCodeStages; st < end - 1; ++st)
+            stage(st, std::false_type{});
+        stage(end - 1, std::true_type{});
     }
-    // lane l holds column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4
+    MOE_WAIT_VMCNT(0);
+    __syncthreads();  // every wave is done with the stages' LDS
+    // lane l holds column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4 of a
+    // subtile: 32 rows at a time go through LDS and leave as 16-byte stores
+    uint8_t* const out = smem + wave * 32 * C::OUT_LD;
+    constexpr int PIECES = NI * 32 / T::VEC;  // 16-byte pieces of a row
+    constexpr int PER = 64 / PIECES;          // rows per store instruction
+    const int c = col0 + wn * NI * 32 + (lane % PIECES) * T::VEC;
 #pragma unroll
-    for (int m = 0; m < MI; ++m)
+    for (int m = 0; m < MI; ++m) {
 #pragma unroll
-        for (int n = 0; n < NI; ++n) {
-            const int c = col0 + (wn * NI + n) * 32 + lr;
+        for (int n = 0; n < NI; ++n)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int r = (wm * MI + m) * 32 + 8 * (i / 4) + 4 * lg + i % 4;
-                if (r < t.rows && c < a.N)
-                    store_y<T>(a, t.row0 + r, c, acc[m][n][i]);
+            for (int i = 0; i < 16; ++i)
+                T::store(reinterpret_cast<char*>(out) + (8 * (i / 4) + 4 * lg + i % 4) * C::OUT_LD +
+                             (n * 32 + lr) * T::SIZE, acc[m][n][i]);
+        // (a wave reads only what it wrote and LDS serves a wave in order;
+        // the compiler must not move the accesses, of other types, past here)
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < 32 / PER; ++q) {
+            const int lrow = q * PER + lane / PIECES;
+            const int r = (wm * MI + m) * 32 + lrow;
+            const char* src = reinterpret_cast<const char*>(out) + lrow * C::OUT_LD + (lane % PIECES) * 16;
+            if (r < t.rows && c < a.N) {
+                char* dst = a.y + (int64_t)(t.row0 + r) * a.y_ld + (int64_t)c * T::SIZE;
+                if (c + T::VEC <= a.N) {
+                    store16(dst, *reinterpret_cast<const rows_u32x4*>(src));
+                } else {
+                    for (int i = 0; i < a.N - c; ++i)
+                        T::store(dst + i * T::SIZE, T::load(src + i * T::SIZE));
+                }
             }
         }
+        asm volatile("" ::: "memory");
+    }
 }
 
 // ------------------------------------------------------------ launchers
@@ -467,22 +582,20 @@ hipError_t launch_few(const MxGemmArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <class T, int WM, int WN, int MI, int NI>
+template <class T, int WM, int WN, int MI, int NI, int NBUF>
 hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
 {
-    constexpr int BM = WM * MI * 32, BN = WN * NI * 32;
-    constexpr int smem = 2 * (BM + BN) * (128 + 8);
-    static_assert(smem <= 160 * 1024, "LDS");
-    const int ct = (a.N + BN - 1) / BN;
-    const unsigned grid = tile_grid(a, BM, ct);
+    using C = TileCfg<T, WM, WN, MI, NI, NBUF>;
+    const int ct = (a.N + C::BN - 1) / C::BN;
+    const unsigned grid = tile_grid(a, C::BM, ct);
     if (!grid)
         return hipErrorInvalidValue;
-    auto kernel = mxfp4_tile<T, WM, WN, MI, NI>;
+    auto kernel = mxfp4_tile<T, WM, WN, MI, NI, NBUF>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WM * WN), smem, s, a, ct);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(C::TH), C::SMEM, s, a, ct);
     return hipGetLastError();
 }
 
@@ -495,8 +608,8 @@ hipError_t launch(const MxGemmArgs& a, hipStream_t s)
     if (mean <= 48)
         return launch_few<T, 2, 2, 8>(a, s);
     if (mean <= 512)
-        return launch_tile<T, 2, 4, 2, 1>(a, s);
-    return launch_tile<T, 2, 4, 4, 2>(a, s);
+        return launch_tile<T, 2, 4, 2, 1, 2>(a, s);
+    return launch_tile<T, 2, 4, 4, 2, 2>(a, s);
 }
 
 }  // namespace

@@ -51,92 +51,87 @@ def ops_lib():
     return _ops
 
 
-def _rows(t, name, device, dtypes=_DTYPES, dtype=None, shape=None):
-    """Checks a matrix of rows; returns its row stride in elements."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
-                         f"{shape if shape is not None else '[rows, width]'}")
-    if t.dtype not in dtypes or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name}: dtype {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    n, w = t.shape
-    if (w > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < w):
+# The raw handle of a device's current stream; torch.cuda.current_stream
+# builds a Stream object for it, a third of a small call's host time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _here(t, stream):
+    """Whether a call with tensor t and this stream argument runs on the
+    current device and its current stream."""
+    if not t.is_cuda:
+        raise ValueError(f"tensors are on {t.device}, expected a GPU")
+    return stream is None and t.get_device() == torch.cuda.current_device()
+
+
+def _elsewhere(fn, t, stream, *args, **kw):
+    """fn(*args, **kw) on t's device and, if one is given, on `stream`, which
+    is then the current one (new outputs belong to it) and is recorded as a
+    user of every tensor of the call."""
+    dev = t.device
+    if stream is None:
+        with torch.cuda.device(dev):
+            return fn(*args, **kw)
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                  else torch.cuda.default_stream(dev))
+    if stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    with torch.cuda.stream(stream):
+        out = fn(*args, **kw)
+    for v in (*args, *kw.values(), *(out if isinstance(out, tuple) else (out,))):
+        if isinstance(v, torch.Tensor):
+            v.record_stream(stream)
+    return out
+
+
+def _rows(t, name, dev, dtype, rows, width):
+    """Checks a [rows, width] matrix of rows; returns its row stride in elements."""
+    if t.dtype is not dtype or t.shape != (rows, width) or t.get_device() != dev:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
+                         f"{(rows, width)} on device {dev}")
+    ld, one = t.stride()
+    if (one != 1 and width > 1) or (ld < width and rows > 1):
         raise ValueError(f"{name}: strides {t.stride()}, expected rows of adjacent elements "
                          "that do not overlap (call .contiguous())")
-    return t.stride(0) if n > 1 else w
+    return ld if rows > 1 else width
 
 
-def _dense(t, name, device, dtype, numel=None, shape=None):
-    """Checks a densely packed tensor; returns its address."""
-    if t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name}: {t.dtype}, strides {t.stride()}, expected contiguous {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if (numel is not None and t.numel() != numel) or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
-                         f"{shape if shape is not None else f'{numel} elements'}")
+def _matrix(t, name, dtypes):
+    """The dtype code and shape of an input matrix of rows."""
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected [rows, width] of "
+                         f"{', '.join(str(d) for d in dtypes)}")
+    return dtypes[t.dtype], t.shape[0], t.shape[1]
+
+
+def _dense(t, name, dev, dtype, n):
+    """Checks a densely packed tensor of n elements (or of shape n); returns its address."""
+    if (t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev or
+            (t.shape != n if isinstance(n, tuple) else t.numel() != n)):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}, "
+                         f"expected contiguous {dtype} of {n if isinstance(n, tuple) else f'{n} elements'} "
+                         f"on device {dev}")
     return t.data_ptr()
 
 
-class _Call:
-    """The device and stream of one call: enters the tensors' device (and,
-    where a stream is given, that stream, so that outputs allocated inside
-    belong to it) and marks the tensors as used there."""
-
-    def __init__(self, t, stream):
-        dev = t.device
-        if dev.type != "cuda":
-            raise ValueError(f"tensors are on {dev}, expected a GPU")
-        self.device = dev
-        self.guard = None
-        if stream is None:
-            if dev.index != torch.cuda.current_device():
-                self.guard = torch.cuda.device(dev)
-            self.stream = None
-        else:
-            if isinstance(stream, int):
-                stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
-                          else torch.cuda.default_stream(dev))
-            if stream.device != dev:
-                raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-            self.stream = stream
-            self.guard = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def handle(self, *tensors):
-        """The stream's handle; the tensors passed are kept for it."""
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        for t in tensors:
-            if t is not None:
-                t.record_stream(self.stream)
-        return self.stream.cuda_stream
-
-
-def _slots(src_row, num_tokens, device):
+def _slots(src_row, num_tokens, dev):
     """Checks src_row [T*K] (any shape); returns its address and K."""
     n = src_row.numel()
-    if num_tokens < 0 or (num_tokens == 0 and n) or (num_tokens and (n == 0 or n % num_tokens)):
+    if num_tokens < 0 or (n % num_tokens or n == 0 if num_tokens else n):
         raise ValueError(f"src_row: {n} slots for {num_tokens} tokens")
-    return _dense(src_row, "src_row", device, torch.int32), max(1, n // max(1, num_tokens))
+    return _dense(src_row, "src_row", dev, torch.int32, n), n // num_tokens if num_tokens else 1
 
 
-def _used(offsets, device):
+def _used(offsets, dev):
     """Address of the used-row count: the last entry of moe_route's offsets."""
     if offsets is None:
         return None
-    if offsets.numel() < 1:
+    n = offsets.numel()
+    if n < 1:
         raise ValueError("offsets: empty")
-    return _dense(offsets, "offsets", device, torch.int32) + 4 * (offsets.numel() - 1)
+    return _dense(offsets, "offsets", dev, torch.int32, n) + 4 * (n - 1)
 
 
 def moe_permute(x, row_src, src_row, offsets, out=None, stream=None):
@@ -144,50 +139,54 @@ def moe_permute(x, row_src, src_row, offsets, out=None, stream=None):
     xp [pool_rows, W] with x[f // K] in row src_row[f], zeros in the padding
     rows below offsets[-1] (offsets None: all rows) and the rows from there on
     left as they were (a new xp: unset).  dtype bf16, f16, f32 or uint8."""
-    with _Call(x, stream) as c:
-        T, W = x.shape if x.dim() == 2 else (0, 0)
-        x_ld = _rows(x, "x", c.device, _DTYPES_U8)
-        src, K = _slots(src_row, T, c.device)
-        R = row_src.numel()
-        if out is None:
-            out = torch.empty(R, W, dtype=x.dtype, device=c.device)
-        ld = _rows(out, "out", c.device, _DTYPES_U8, x.dtype, (R, W))
-        _check(ops_lib().moe_permute(
-            T, K, R, W, _DTYPES_U8[x.dtype], x.data_ptr(), x_ld,
-            _dense(row_src, "row_src", c.device, torch.int32), src, _used(offsets, c.device),
-            out.data_ptr(), ld, c.handle(x, row_src, src_row, offsets, out)), "moe_permute")
-    return out
-
-
-def _token_sums(fn, what, rows, src_row, num_tokens, w, out, stream):
-    with _Call(rows, stream) as c:
-        ld = _rows(rows, "rows", c.device)
-        R, W = rows.shape
-        src, K = _slots(src_row, num_tokens, c.device)
-        if out is None:
-            out = torch.empty(num_tokens, W, dtype=rows.dtype, device=c.device)
-        out_ld = _rows(out, "out", c.device, _DTYPES, rows.dtype, (num_tokens, W))
-        args = [num_tokens, K, R, W, _DTYPES[rows.dtype], rows.data_ptr(), ld, src]
-        if fn == "moe_unpermute":
-            args.append(None if w is None else
-                        _dense(w, "topk_w", c.device, torch.float32, num_tokens * K))
-        _check(getattr(ops_lib(), fn)(*args, out.data_ptr(), out_ld,
-                                      c.handle(rows, src_row, w, out)), what)
+    if not _here(x, stream):
+        return _elsewhere(moe_permute, x, stream, x, row_src, src_row, offsets, out)
+    dev = x.get_device()
+    dt, T, W = _matrix(x, "x", _DTYPES_U8)
+    src, K = _slots(src_row, T, dev)
+    R = row_src.numel()
+    if out is None:
+        out = torch.empty(R, W, dtype=x.dtype, device=x.device)
+    _check(ops_lib().moe_permute(
+        T, K, R, W, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, T, W),
+        _dense(row_src, "row_src", dev, torch.int32, R), src, _used(offsets, dev),
+        out.data_ptr(), _rows(out, "out", dev, x.dtype, R, W), _raw_stream(dev)), "moe_permute")
     return out
 
 
 def moe_permute_bwd(dxp, src_row, num_tokens, out=None, stream=None):
     """Gradient of moe_permute: dx [T, W], each token's sum of its slots' rows
     of dxp [pool_rows, W] (f32 sums, rounded once)."""
-    return _token_sums("moe_permute_bwd", "moe_permute_bwd", dxp, src_row, num_tokens, None, out,
-                       stream)
+    if not _here(dxp, stream):
+        return _elsewhere(moe_permute_bwd, dxp, stream, dxp, src_row, num_tokens, out)
+    dev = dxp.get_device()
+    dt, R, W = _matrix(dxp, "dxp", _DTYPES)
+    src, K = _slots(src_row, num_tokens, dev)
+    if out is None:
+        out = torch.empty(num_tokens, W, dtype=dxp.dtype, device=dxp.device)
+    _check(ops_lib().moe_permute_bwd(
+        num_tokens, K, R, W, dt, dxp.data_ptr(), _rows(dxp, "dxp", dev, dxp.dtype, R, W), src,
+        out.data_ptr(), _rows(out, "out", dev, dxp.dtype, num_tokens, W), _raw_stream(dev)),
+        "moe_permute_bwd")
+    return out
 
 
 def moe_unpermute(yp, src_row, num_tokens, topk_w=None, out=None, stream=None):
     """Expert rows yp [pool_rows, W] back to tokens: y [T, W], each token's sum
     of topk_w[t, j] (f32; None: 1) times its slots' rows."""
-    return _token_sums("moe_unpermute", "moe_unpermute", yp, src_row, num_tokens, topk_w, out,
-                       stream)
+    if not _here(yp, stream):
+        return _elsewhere(moe_unpermute, yp, stream, yp, src_row, num_tokens, topk_w, out)
+    dev = yp.get_device()
+    dt, R, W = _matrix(yp, "yp", _DTYPES)
+    src, K = _slots(src_row, num_tokens, dev)
+    if out is None:
+        out = torch.empty(num_tokens, W, dtype=yp.dtype, device=yp.device)
+    _check(ops_lib().moe_unpermute(
+        num_tokens, K, R, W, dt, yp.data_ptr(), _rows(yp, "yp", dev, yp.dtype, R, W), src,
+        None if topk_w is None else _dense(topk_w, "topk_w", dev, torch.float32, num_tokens * K),
+        out.data_ptr(), _rows(out, "out", dev, yp.dtype, num_tokens, W), _raw_stream(dev)),
+        "moe_unpermute")
+    return out
 
 
 def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, dw=None,
@@ -196,63 +195,64 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
     [T, K]); dyp's padding rows below offsets[-1] are zeros, its rows from
     there on left as they were.  need_dyp / need_dw False: that one is None
     (without need_dw, yp is not read and may be None)."""
-    with _Call(dy, stream) as c:
-        ld = _rows(dy, "dy", c.device)
-        T, W = dy.shape
-        src, K = _slots(src_row, T, c.device)
-        rs = _dense(row_src, "row_src", c.device, torch.int32)
-        R = row_src.numel()
-        yp_ld = dyp_ld = 0
-        if need_dw:
-            yp_ld = _rows(yp, "yp", c.device, _DTYPES, dy.dtype, (R, W))
-            if dw is None:
-                dw = torch.empty(T, K, dtype=torch.float32, device=c.device)
-            _dense(dw, "dw", c.device, torch.float32, T * K)
-        if need_dyp:
-            if dyp is None:
-                dyp = torch.empty(R, W, dtype=dy.dtype, device=c.device)
-            dyp_ld = _rows(dyp, "dyp", c.device, _DTYPES, dy.dtype, (R, W))
-        w = None if topk_w is None else _dense(topk_w, "topk_w", c.device, torch.float32, T * K)
-        _check(ops_lib().moe_unpermute_bwd(
-            T, K, R, W, _DTYPES[dy.dtype], dy.data_ptr(), ld,
-            yp.data_ptr() if need_dw else None, yp_ld, rs, src, _used(offsets, c.device), w,
-            dyp.data_ptr() if need_dyp else None, dyp_ld, dw.data_ptr() if need_dw else None,
-            c.handle(dy, yp if need_dw else None, row_src, src_row, offsets, topk_w, dyp, dw)),
-            "moe_unpermute_bwd")
+    if not _here(dy, stream):
+        return _elsewhere(moe_unpermute_bwd, dy, stream, dy, yp, row_src, src_row, offsets, topk_w,
+                          dyp, dw, need_dyp, need_dw)
+    dev = dy.get_device()
+    dt, T, W = _matrix(dy, "dy", _DTYPES)
+    src, K = _slots(src_row, T, dev)
+    R = row_src.numel()
+    yp_at = dyp_at = dw_at = None
+    yp_ld = dyp_ld = 0
+    if need_dw:
+        yp_at, yp_ld = yp.data_ptr(), _rows(yp, "yp", dev, dy.dtype, R, W)
+        if dw is None:
+            dw = torch.empty(T, K, dtype=torch.float32, device=dy.device)
+        dw_at = _dense(dw, "dw", dev, torch.float32, T * K)
+    if need_dyp:
+        if dyp is None:
+            dyp = torch.empty(R, W, dtype=dy.dtype, device=dy.device)
+        dyp_at, dyp_ld = dyp.data_ptr(), _rows(dyp, "dyp", dev, dy.dtype, R, W)
+    _check(ops_lib().moe_unpermute_bwd(
+        T, K, R, W, dt, dy.data_ptr(), _rows(dy, "dy", dev, dy.dtype, T, W), yp_at, yp_ld,
+        _dense(row_src, "row_src", dev, torch.int32, R), src, _used(offsets, dev),
+        None if topk_w is None else _dense(topk_w, "topk_w", dev, torch.float32, T * K),
+        dyp_at, dyp_ld, dw_at, _raw_stream(dev)), "moe_unpermute_bwd")
     return (dyp if need_dyp else None), (dw if need_dw else None)
 
 
 def moe_quantize_mxfp4(x, codes=None, sf=None, stream=None):
     """Rows x [M, C] (bf16, f16 or f32, C a multiple of 32) to packed e2m1
     codes uint8 [M, C/2] and UE8M0 scale codes uint8 [M, C/32]."""
-    with _Call(x, stream) as c:
-        ld = _rows(x, "x", c.device)
-        M, C = x.shape
-        if codes is None:
-            codes = torch.empty(M, C // 2, dtype=torch.uint8, device=c.device)
-        if sf is None:
-            sf = torch.empty(M, C // 32, dtype=torch.uint8, device=c.device)
-        _check(ops_lib().moe_quantize_mxfp4(
-            M, C, _DTYPES[x.dtype], x.data_ptr(), ld,
-            _dense(codes, "codes", c.device, torch.uint8, shape=(M, C // 2)),
-            _dense(sf, "sf", c.device, torch.uint8, shape=(M, C // 32)),
-            c.handle(x, codes, sf)), "moe_quantize_mxfp4")
+    if not _here(x, stream):
+        return _elsewhere(moe_quantize_mxfp4, x, stream, x, codes, sf)
+    dev, u8 = x.get_device(), torch.uint8
+    dt, M, C = _matrix(x, "x", _DTYPES)
+    if codes is None:
+        codes = torch.empty(M, C // 2, dtype=u8, device=x.device)
+    if sf is None:
+        sf = torch.empty(M, C // 32, dtype=u8, device=x.device)
+    _check(ops_lib().moe_quantize_mxfp4(
+        M, C, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, M, C),
+        _dense(codes, "codes", dev, u8, (M, C // 2)), _dense(sf, "sf", dev, u8, (M, C // 32)),
+        _raw_stream(dev)), "moe_quantize_mxfp4")
     return codes, sf
 
 
 def moe_dequantize_mxfp4(codes, sf, dtype=torch.bfloat16, out=None, stream=None):
     """The values [M, C] of e2m1 codes [M, C/2] and UE8M0 codes [M, C/32]."""
-    with _Call(codes, stream) as c:
-        if codes.dim() != 2 or dtype not in _DTYPES:
-            raise ValueError(f"codes: shape {tuple(codes.shape)}; dtype {dtype}")
-        M, C = codes.shape[0], 2 * codes.shape[1]
-        if out is None:
-            out = torch.empty(M, C, dtype=dtype, device=c.device)
-        ld = _rows(out, "out", c.device, _DTYPES, dtype, (M, C))
-        _check(ops_lib().moe_dequantize_mxfp4(
-            M, C, _DTYPES[dtype], _dense(codes, "codes", c.device, torch.uint8),
-            _dense(sf, "sf", c.device, torch.uint8, shape=(M, C // 32)), out.data_ptr(), ld,
-            c.handle(codes, sf, out)), "moe_dequantize_mxfp4")
+    if not _here(codes, stream):
+        return _elsewhere(moe_dequantize_mxfp4, codes, stream, codes, sf, dtype, out)
+    dev, u8 = codes.get_device(), torch.uint8
+    if codes.dim() != 2 or dtype not in _DTYPES:
+        raise ValueError(f"codes: shape {tuple(codes.shape)}; dtype {dtype}")
+    M, C = codes.shape[0], 2 * codes.shape[1]
+    if out is None:
+        out = torch.empty(M, C, dtype=dtype, device=codes.device)
+    _check(ops_lib().moe_dequantize_mxfp4(
+        M, C, _DTYPES[dtype], _dense(codes, "codes", dev, u8, (M, C // 2)),
+        _dense(sf, "sf", dev, u8, (M, C // 32)), out.data_ptr(),
+        _rows(out, "out", dev, dtype, M, C), _raw_stream(dev)), "moe_dequantize_mxfp4")
     return out
 
 
@@ -264,30 +264,28 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
     whole lengths): expert e's rows offsets[e] .. + counts[e], the other rows
     of y left as they were (a new y: unset).  y's type: out's, else dtype,
     else bf16."""
-    with _Call(a, stream) as c:
-        if a.dim() != 2 or b.dim() != (2 if offsets is None else 3):
-            raise ValueError(f"a: shape {tuple(a.shape)}, b: shape {tuple(b.shape)}, expected "
-                             "[rows, k/2] and [n, k/2], or [experts, n, k/2] with offsets")
-        if offsets is None and counts is not None:
-            raise ValueError("counts without offsets")
-        R, K, N = a.shape[0], 2 * a.shape[1], b.shape[-2]
-        E = 1 if offsets is None else b.shape[0]
-        lead = () if offsets is None else (E,)
-        if dtype is None:
-            dtype = torch.bfloat16 if out is None else out.dtype
-        if dtype not in _DTYPES:
-            raise ValueError(f"dtype {dtype}")
-        if out is None:
-            out = torch.empty(R, N, dtype=dtype, device=c.device)
-        ld = _rows(out, "out", c.device, _DTYPES, dtype, (R, N))
-        u8, i32 = torch.uint8, torch.int32
-        _check(ops_lib().moe_gemm_mxfp4(
-            E, R, N, K, _DTYPES[dtype], _dense(a, "a", c.device, u8),
-            _dense(a_sf, "a_sf", c.device, u8, shape=(R, K // 32)),
-            _dense(b, "b", c.device, u8, shape=lead + (N, K // 2)),
-            _dense(b_sf, "b_sf", c.device, u8, shape=lead + (N, K // 32)),
-            None if offsets is None else _dense(offsets, "offsets", c.device, i32, E + 1),
-            None if counts is None else _dense(counts, "counts", c.device, i32, E),
-            out.data_ptr(), ld, c.handle(a, a_sf, b, b_sf, offsets, counts, out)),
-            "moe_gemm_mxfp4")
+    if not _here(a, stream):
+        return _elsewhere(moe_gemm_mxfp4, a, stream, a, a_sf, b, b_sf, offsets, counts, dtype, out)
+    dev, u8, i32 = a.get_device(), torch.uint8, torch.int32
+    if a.dim() != 2 or b.dim() != (2 if offsets is None else 3):
+        raise ValueError(f"a: shape {tuple(a.shape)}, b: shape {tuple(b.shape)}, expected "
+                         "[rows, k/2] and [n, k/2], or [experts, n, k/2] with offsets")
+    if offsets is None and counts is not None:
+        raise ValueError("counts without offsets")
+    R, k2 = a.shape
+    N, nb = b.shape[-2], k2 // 16
+    E, lead = (1, ()) if offsets is None else (b.shape[0], (b.shape[0],))
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype {dtype}")
+    if out is None:
+        out = torch.empty(R, N, dtype=dtype, device=a.device)
+    _check(ops_lib().moe_gemm_mxfp4(
+        E, R, N, 2 * k2, _DTYPES[dtype], _dense(a, "a", dev, u8, (R, k2)),
+        _dense(a_sf, "a_sf", dev, u8, (R, nb)), _dense(b, "b", dev, u8, lead + (N, k2)),
+        _dense(b_sf, "b_sf", dev, u8, lead + (N, nb)),
+        None if offsets is None else _dense(offsets, "offsets", dev, i32, E + 1),
+        None if counts is None else _dense(counts, "counts", dev, i32, E),
+        out.data_ptr(), _rows(out, "out", dev, dtype, R, N), _raw_stream(dev)), "moe_gemm_mxfp4")
     return out
