@@ -385,4 +385,5 @@ def __getattr__(name):
 
 _OPS_NAMES = ("moe_permute", "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd",
               "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4",
+              "moe_gemm_mxfp4_info",
               "MOE_DTYPE_BF16", "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_U8")

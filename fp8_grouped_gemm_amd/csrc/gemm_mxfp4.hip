@@ -14,6 +14,7 @@
 // instruction's 4 (2), and that block's UE8M0 code in the byte of its scale
 // register that the instruction selects.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "../../include/moe_ops.h"
@@ -42,57 +43,21 @@ __device__ __forceinline__ void segment(const MxGemmArgs& a, int e, int& first, 
     n = max(0, min(n, a.R - first));
 }
 
-// Row tiles of BM rows over all segments, in expert order: how many there
-// are, and (by find_tile) which one is number `want`.  A wave looks at 64
-// experts at a time; every wave of a workgroup does so for itself.
-template <int BM>
-__device__ __forceinline__ int count_tiles(const MxGemmArgs& a, int lane)
+// Inclusive sum over the lanes below and including this one.
+__device__ __forceinline__ int lane_sums(int v, int lane)
 {
-    int total = 0;
-    for (int e = lane; e < a.E; e += 64) {
-        int first, n;
-        segment(a, e, first, n);
-        total += (n + BM - 1) / BM;
-    }
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        total += __shfl_xor(total, d);
-    return __builtin_amdgcn_readfirstlane(total);
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d)
+            v += u;
+    }
+    return v;
 }
 
-template <int BM>
-__device__ __forceinline__ RowTile find_tile(const MxGemmArgs& a, int want, int lane)
-{
-    int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        const int e = e0 + lane;
-        int first = 0, n = 0;
-        if (e < a.E)
-            segment(a, e, first, n);
-        const int tiles = (n + BM - 1) / BM;
-        int incl = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(incl, d);
-            if (lane >= d)
-                incl += v;
-        }
-        const uint64_t past = __ballot(before + incl > want);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            const int skip = (want - before - __shfl(incl - tiles, l)) * BM;
-            RowTile t;
-            t.e = e0 + l;
-            t.row0 = __builtin_amdgcn_readfirstlane(__shfl(first, l) + skip);
-            t.rows = __builtin_amdgcn_readfirstlane(min(BM, __shfl(n, l) - skip));
-            return t;
-        }
-        before += __shfl(incl, 63);
-    }
-    return {0, 0, 0};
-}
-
-// Row tile and column tile of workgroup `wg`.  Workgroups go to the 8 XCDs
+// Row tile and column tile of this workgroup.  Row tiles of BM rows are
+// numbered over all segments in expert order; a wave looks at 64 experts at
+// a time, and every wave does so for itself.  Workgroups go to the 8 XCDs
 // round-robin, each XCD takes a contiguous share of the tiles, and tiles run
 // in bands of up to 8 row tiles, column by column, so that the tiles an XCD
 // works on at one time share rows of a and of b in its L2.
@@ -100,7 +65,20 @@ template <int BM>
 __device__ __forceinline__ RowTile pick_tile(const MxGemmArgs& a, int col_tiles, int lane, int& ct)
 {
     constexpr int kBand = 8;
-    const int row_tiles = a.offsets ? count_tiles<BM>(a, lane) : (a.R + BM - 1) / BM;
+    const bool grouped = a.offsets != nullptr;
+    int first = 0, n = 0, tiles = 0, upto = 0;  // of the lane's expert in the last 64 looked at
+    int row_tiles = (a.R + BM - 1) / BM;
+    if (grouped) {
+        row_tiles = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            n = 0;
+            if (e0 + lane < a.E)
+                segment(a, e0 + lane, first, n);
+            tiles = (n + BM - 1) / BM;
+            upto = lane_sums(tiles, lane);
+            row_tiles += __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
     const int total = row_tiles * col_tiles;
     const int share = (total + 7) / 8;
     const int i = blockIdx.x / 8, at = (blockIdx.x % 8) * share + i;
@@ -110,15 +88,36 @@ __device__ __forceinline__ RowTile pick_tile(const MxGemmArgs& a, int col_tiles,
     const int tall = min(kBand, row_tiles - band * kBand);
     ct = in / tall;
     const int rt = band * kBand + in - ct * tall;
-    if (a.offsets)
-        return find_tile<BM>(a, rt, lane);
-    return {0, rt * BM, min(BM, a.R - rt * BM)};
+    if (!grouped)
+        return {0, rt * BM, min(BM, a.R - rt * BM)};
+    int before = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        if (a.E > 64) {  // (up to 64 experts: still in the registers)
+            n = 0;
+            if (e0 + lane < a.E)
+                segment(a, e0 + lane, first, n);
+            tiles = (n + BM - 1) / BM;
+            upto = lane_sums(tiles, lane);
+        }
+        const uint64_t past = __ballot(before + upto > rt);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const int skip = (rt - before - __builtin_amdgcn_readlane(upto - tiles, l)) * BM;
+            return {e0 + l, __builtin_amdgcn_readlane(first, l) + skip,
+                    min(BM, __builtin_amdgcn_readlane(n, l) - skip)};
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return {0, 0, 0};
 }
 
-template <class T>
-__device__ __forceinline__ void store_y(const MxGemmArgs& a, int row, int col, float v)
+// A buffer resource of `bytes` bytes at p (both wave-uniform); what lies past
+// them reads as zeros, an offset of kOutside among it.
+constexpr uint32_t kOutside = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t byte_rsrc(const uint8_t* p, uint32_t bytes)
 {
-    T::store(a.y + (int64_t)row * a.y_ld + (int64_t)col * T::SIZE, v);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, (int)bytes, 0x00020000);
 }
 
 }  // namespace
@@ -128,17 +127,18 @@ __device__ __forceinline__ void store_y(const MxGemmArgs& a, int row, int col, f
 // 16 MT rows x 16 NT columns per workgroup of WV waves that split K: wave w
 // takes the 256-wide K steps w, w + WV, ... (so the workgroup reads WV * 128
 // consecutive bytes of each weight row at a time), straight from memory into
-// MFMA operands, and the waves' sums meet in LDS in wave order.  A step is
-// two MFMAs per subtile pair: lane group g supplies K blocks 2g and 2g + 1
-// of the step's 8, so its two 16-byte loads are adjacent and the four groups
-// read one whole 128-byte line of each row.
+// MFMA operands, D steps of each wave in flight, and the waves' sums meet in
+// LDS in wave order.  A step is two MFMAs per subtile pair: lane group g
+// supplies K blocks 2 g and 2 g + 1 of the step's 8, so its two 16-byte loads
+// are adjacent and the four groups read one whole 128-byte line of each row.
+// Steps past the end are loads from outside the buffer resource: zeros.
 template <int MT, int NT>
 struct Step {
     uint4 a[MT][2], b[NT][2];
     int sa[MT], sb[NT];  // codes of the two blocks in bytes 0 and 1
 };
 
-template <class T, int MT, int NT, int WV>
+template <class T, int MT, int NT, int WV, int D>
 __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tiles)
 {
     constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -150,52 +150,36 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
     if (t.rows <= 0)
         return;
     const int lr = lane & 15, lg = lane >> 4;
-    const int nb = a.K / 32;  // K blocks
-    const int col0 = ct * BN;
-    // Rows and columns past the tile's repeat its last one (never stored).
-    const uint8_t *pa[MT], *pb[NT], *psa[MT], *psb[NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t r = t.row0 + min(16 * m + lr, t.rows - 1);
-        pa[m] = a.a + r * (a.K / 2);
-        psa[m] = a.a_sf + r * nb;
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int64_t c = (int64_t)t.e * a.N + min(col0 + 16 * n + lr, a.N - 1);
-        pb[n] = a.b + c * (a.K / 2);
-        psb[n] = a.b_sf + c * nb;
-    }
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int nb = a.K / 32, full = nb / 8;  // K blocks, whole steps
+    const uint32_t pitch = a.K / 2;
+    const int col0 = ct * BN, cols = min(BN, a.N - col0);
+    const int64_t b0 = (int64_t)t.e * a.N + col0;
+    const auto ra = byte_rsrc(a.a + (int64_t)t.row0 * pitch, t.rows * pitch);
+    const auto rb = byte_rsrc(a.b + b0 * pitch, cols * pitch);
+    const auto rsa = byte_rsrc(a.a_sf + (int64_t)t.row0 * nb, t.rows * nb);
+    const auto rsb = byte_rsrc(a.b_sf + b0 * nb, cols * nb);
+    // (rows and columns past the tile lie outside the resources)
+    auto load = [](__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+        const u4 v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+        return make_uint4(v.x, v.y, v.z, v.w);
+    };
     auto fetch = [&](Step<MT, NT>& s, int step) {
-        const int blk = step * 8 + 2 * lg;
-        if (step * 8 + 8 <= nb) {
+        const uint32_t blk = step * 8 + 2 * lg;
+        const bool in = step < full;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                s.b[n][0] = *reinterpret_cast<const uint4*>(pb[n] + blk * 16);
-                s.b[n][1] = *reinterpret_cast<const uint4*>(pb[n] + blk * 16 + 16);
-                s.sb[n] = psb[n][blk] | (psb[n][blk + 1] << 8);
-            }
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t r = 16 * n + lr, off = in ? r * pitch + blk * 16 : kOutside;
+            s.b[n][0] = load(rb, off);
+            s.b[n][1] = load(rb, off + 16);
+            s.sb[n] = __builtin_amdgcn_raw_buffer_load_b16(rsb, (int)(in ? r * nb + blk : kOutside), 0, 0);
+        }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                s.a[m][0] = *reinterpret_cast<const uint4*>(pa[m] + blk * 16);
-                s.a[m][1] = *reinterpret_cast<const uint4*>(pa[m] + blk * 16 + 16);
-                s.sa[m] = psa[m][blk] | (psa[m][blk + 1] << 8);
-            }
-        } else {  // the step K ends in: blocks past it are zeros with scale 1
-            const bool in0 = blk < nb, in1 = blk + 1 < nb;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                s.b[n][0] = in0 ? *reinterpret_cast<const uint4*>(pb[n] + blk * 16) : zero;
-                s.b[n][1] = in1 ? *reinterpret_cast<const uint4*>(pb[n] + blk * 16 + 16) : zero;
-                s.sb[n] = (in0 ? psb[n][blk] : 127) | ((in1 ? psb[n][blk + 1] : 127) << 8);
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                s.a[m][0] = in0 ? *reinterpret_cast<const uint4*>(pa[m] + blk * 16) : zero;
-                s.a[m][1] = in1 ? *reinterpret_cast<const uint4*>(pa[m] + blk * 16 + 16) : zero;
-                s.sa[m] = (in0 ? psa[m][blk] : 127) | ((in1 ? psa[m][blk + 1] : 127) << 8);
-            }
+        for (int m = 0; m < MT; ++m) {
+            const uint32_t r = 16 * m + lr, off = in ? r * pitch + blk * 16 : kOutside;
+            s.a[m][0] = load(ra, off);
+            s.a[m][1] = load(ra, off + 16);
+            s.sa[m] = __builtin_amdgcn_raw_buffer_load_b16(rsa, (int)(in ? r * nb + blk : kOutside), 0, 0);
         }
     };
     v4f acc[MT][NT];
@@ -215,24 +199,40 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
                     e2m1_operand(s.a[m][1]), e2m1_operand(s.b[n][1]), acc[m][n], 4, 4, 1, s.sa[m], 1, s.sb[n]);
             }
     };
-    const int steps = (nb + 7) / 8;
-    {
-        Step<MT, NT> s0, s1;
-        int i = wave;
-        if (i < steps)
-            fetch(s0, i);
-        while (i < steps) {
-            if (i + WV < steps)
-                fetch(s1, i + WV);
-            mul(s0);
-            i += WV;
-            if (i >= steps)
-                break;
-            if (i + WV < steps)
-                fetch(s0, i + WV);
-            mul(s1);
-            i += WV;
+    Step<MT, NT> s[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        fetch(s[d], wave + d * WV);
+    for (int i = wave; i < full; i += D * WV) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            mul(s[d]);
+            fetch(s[d], i + (D + d) * WV);
         }
+    }
+    if (nb % 8 != 0 && wave == full % WV) {  // the step K ends in: code by code
+        const uint32_t blk = full * 8 + 2 * lg;
+        const bool in0 = (int)blk < nb, in1 = (int)blk + 1 < nb;
+        auto code2 = [&](__amdgpu_buffer_rsrc_t r, uint32_t off) {
+            const int lo = __builtin_amdgcn_raw_buffer_load_b8(r, (int)(in0 ? off : kOutside), 0, 0);
+            const int hi = __builtin_amdgcn_raw_buffer_load_b8(r, (int)(in1 ? off + 1 : kOutside), 0, 0);
+            return lo | (hi << 8);
+        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t r = 16 * n + lr, off = r * pitch + blk * 16;
+            s[0].b[n][0] = load(rb, in0 ? off : kOutside);
+            s[0].b[n][1] = load(rb, in1 ? off + 16 : kOutside);
+            s[0].sb[n] = code2(rsb, r * nb + blk);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const uint32_t r = 16 * m + lr, off = r * pitch + blk * 16;
+            s[0].a[m][0] = load(ra, in0 ? off : kOutside);
+            s[0].a[m][1] = load(ra, in1 ? off + 16 : kOutside);
+            s[0].sa[m] = code2(rsa, r * nb + blk);
+        }
+        mul(s[0]);
     }
     // lane l holds column l % 16, rows 4 (l / 16) + i of each subtile
 #pragma unroll
@@ -245,13 +245,13 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
     __syncthreads();
     for (int c = threadIdx.x; c < BM * BN; c += 64 * WV) {
         const int m = c / BN, n = c % BN;
-        if (m >= t.rows || col0 + n >= a.N)
+        if (m >= t.rows || n >= cols)
             continue;
         float v = part[0][m][n];
 #pragma unroll
         for (int w = 1; w < WV; ++w)
             v += part[w][m][n];
-        store_y<T>(a, t.row0 + m, col0 + n, v);
+        T::store(a.y + (int64_t)(t.row0 + m) * a.y_ld + (int64_t)(col0 + n) * T::SIZE, v);
     }
 }
 
@@ -281,7 +281,6 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
 // time; a byte permute of a row's 8 codes of one stage gives the MFMAs' scale
 // register for its four steps (lane group g takes codes 2 s + g, step s byte
 // s).  Codes past the end of K are 127, scale 1.
-typedef int v4i __attribute__((ext_vector_type(4)));
 constexpr int kCodeStages = 4;  // stages per load of scale codes
 
 template <class T, int WM, int WN, int MI, int NI, int NBUF>
@@ -300,21 +299,8 @@ struct TileCfg {
     static_assert(SMEM <= 160 * 1024 && W * 32 * OUT_LD <= SMEM, "LDS");
 };
 
-// A buffer resource of `bytes` bytes at p (both wave-uniform); what lies past
-// them reads as zeros.
-__device__ __forceinline__ v4i byte_rsrc(const uint8_t* p, uint32_t bytes)
-{
-    const uint64_t b = reinterpret_cast<uint64_t>(p);
-    v4i r;
-    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
-    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32) & 0xFFFF);
-    r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-    r[3] = 0x00020000;
-    return r;
-}
-
 // 16 bytes per lane from byte `off` of the resource to LDS at lds + 16 * lane.
-__device__ __forceinline__ void dma16_rsrc(const v4i& r, uint32_t off, uint32_t lds)
+__device__ __forceinline__ void dma16_rsrc(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r),
                  "s"(__builtin_amdgcn_readfirstlane(lds))
@@ -337,8 +323,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
     const int col0 = ct * BN, cols = min(BN, a.N - col0);
     const int nb = a.K / 32, stages = (nb + 7) / 8;
     const uint32_t pitch = a.K / 2;
-    const v4i ra = byte_rsrc(a.a + (int64_t)t.row0 * pitch, t.rows * pitch);
-    const v4i rb = byte_rsrc(a.b + ((int64_t)t.e * a.N + col0) * pitch, cols * pitch);
+    const auto ra = byte_rsrc(a.a + (int64_t)t.row0 * pitch, t.rows * pitch);
+    const auto rb = byte_rsrc(a.b + ((int64_t)t.e * a.N + col0) * pitch, cols * pitch);
     const uint8_t* const asf = a.a_sf + (int64_t)t.row0 * nb;
     const uint8_t* const bsf = a.b_sf + ((int64_t)t.e * a.N + col0) * nb;
 
@@ -351,7 +337,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
     auto copy = [&](int st, int buf, int q) {
         constexpr int QA = BM / 8 / W;  // copies of a's rows
         const uint32_t at = off0 + (q < QA ? q : q - QA) * (8 * W) * pitch + st * 128;
-        dma16_rsrc(q < QA ? ra : rb, st * 8 + chunk < nb ? at : 0x80000000u,
+        dma16_rsrc(q < QA ? ra : rb, st * 8 + chunk < nb ? at : kOutside,
                    lds0 + buf * C::STAGE + q * W * 1024);
     };
     // Scale codes: thread i takes rows i, i + TH, ... of the ROWS.
@@ -453,13 +439,13 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
     constexpr int HALF = C::COPIES / 2;
 
     // prologue: the first codes, stages 0 .. NBUF - 2 and half of the next
-    fetch_codes(0);
-    leave_codes(0);
 #pragma unroll
     for (int st = 0; st < NBUF - 1; ++st)
 #pragma unroll
         for (int q = 0; q < C::COPIES; ++q)
             copy(st, st, q);
+    fetch_codes(0);
+    leave_codes(0);
     MOE_WAIT_VMCNT((NBUF - 2) * C::COPIES);
     __syncthreads();
 #pragma unroll
@@ -571,14 +557,14 @@ unsigned tile_grid(const MxGemmArgs& a, int bm, int col_tiles)
     return g < (INT64_C(1) << 31) ? (unsigned)g : 0u;
 }
 
-template <class T, int MT, int NT, int WV>
+template <class T, int MT, int NT, int WV, int D>
 hipError_t launch_few(const MxGemmArgs& a, hipStream_t s)
 {
     const int ct = (a.N + 16 * NT - 1) / (16 * NT);
     const unsigned grid = tile_grid(a, 16 * MT, ct);
     if (!grid)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((mxfp4_rows<T, MT, NT, WV>), dim3(grid), dim3(64 * WV), 0, s, a, ct);
+    hipLaunchKernelGGL((mxfp4_rows<T, MT, NT, WV, D>), dim3(grid), dim3(64 * WV), 0, s, a, ct);
     return hipGetLastError();
 }
 
@@ -599,20 +585,87 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
+// The kernel a call takes: the one whose estimated time is least.  A kernel's
+// workgroups run `per_cu` to a compute unit, each fix + step * (256-wide K
+// steps) microseconds at that occupancy and fix1 + step1 * steps alone on its
+// unit, in whole rounds over the 256 units.  The figures are fits to a sweep
+// of 34 shapes (rows 1 to 12288, n and k 512 to 8192, 1 to 64 experts), where
+// the choice is within 10 % of the best of 16 tile shapes; some of its points,
+// us per call (7 us of them the host's share):
+//   rows x n x k (experts)   16x16  32x16  32x64  32x128  64x128  128^2  256^2
+//   1 x 4096 x 7168            7.7    7.4   11.1    17.1    13.2   21.3   37.3
+//   32 x 4096 x 4096           8.5    7.3    7.9     8.8     8.8   11.6   23.9
+//   128 x 4096 x 7168         43.8   33.8   12.1    18.7    15.3   24.5   39.7
+//   512 x 4096 x 4096          101   76.1   18.8    14.2    11.6   16.1   26.7
+//   2048 x 4096 x 4096         397    299   66.9    47.8    40.4   28.4   30.9
+//   4096 x 4096 x 4096         791    596    128    94.4    80.1   54.9   41.3
+//   32 x 4096 x 4096 (32)     52.2   71.5   36.8    31.5    39.5   46.3   65.2
+//   768 x 4096 x 4096 (32)     207    197   71.1    63.6    70.3   64.5   83.0
+//   3072 x 4096 x 4096 (32)    655    558    156     117     111   91.2    102
+//   12288 x 4096 x 4096 (32)  2457   2018    494     335     317    204    174
+struct Choice {
+    int bm, bn, per_cu;
+    double fix, step, fix1, step1;
+};
+constexpr Choice kChoices[] = {
+    {16, 16, 2, 2.0, 0.22, 2.0, 0.12},  {32, 16, 2, 2.0, 0.31, 2.0, 0.16},
+    {32, 64, 2, 1.5, 0.40, 1.5, 0.28},  {32, 128, 3, 3.0, 0.83, 2.0, 0.40},
+    {64, 128, 1, 2.5, 0.47, 2.5, 0.36}, {128, 128, 2, 5.0, 1.30, 4.0, 0.75},
+    {256, 256, 1, 6.0, 2.10, 6.0, 2.10},
+};
+
+// Row tiles of bm rows: exact for a dense product; over segments, whose
+// lengths only the device knows, the routed experts at least and half a tile
+// for each beyond the full ones.
+double row_tiles(int E, int R, bool grouped, int bm)
+{
+    if (!grouped)
+        return (R + bm - 1) / bm;
+    const double routed = E * (1.0 - std::exp(-(double)R / E));
+    return std::max(routed, (double)R / bm + 0.5 * routed);
+}
+
+int choose(int E, int R, int N, int K, bool grouped)
+{
+    constexpr int kUnits = 256;
+    const double steps = (K + 255) / 256;
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < (int)(sizeof(kChoices) / sizeof(kChoices[0])); ++i) {
+        const Choice& c = kChoices[i];
+        const double tiles = row_tiles(E, R, grouped, c.bm) * ((N + c.bn - 1) / c.bn);
+        const double us = tiles <= kUnits ? c.fix1 + c.step1 * steps
+                                          : std::ceil(tiles / (kUnits * c.per_cu)) * (c.fix + c.step * steps);
+        if (i == 0 || us < least) {
+            best = i;
+            least = us;
+        }
+    }
+    return best;
+}
+
 template <class T>
 hipError_t launch(const MxGemmArgs& a, hipStream_t s)
 {
-    const double mean = (double)a.R / a.E;
-    if (mean <= 16)
-        return launch_few<T, 1, 1, 8>(a, s);
-    if (mean <= 48)
-        return launch_few<T, 2, 2, 8>(a, s);
-    if (mean <= 512)
-        return launch_tile<T, 2, 4, 2, 1, 2>(a, s);
-    return launch_tile<T, 2, 4, 4, 2, 2>(a, s);
+    switch (choose(a.E, a.R, a.N, a.K, a.offsets != nullptr)) {
+    case 0: return launch_few<T, 1, 1, 8, 2>(a, s);
+    case 1: return launch_few<T, 2, 1, 8, 2>(a, s);
+    case 2: return launch_tile<T, 1, 2, 1, 1, 4>(a, s);
+    case 3: return launch_tile<T, 1, 4, 1, 1, 2>(a, s);
+    case 4: return launch_tile<T, 2, 4, 1, 1, 3>(a, s);
+    case 5: return launch_tile<T, 2, 2, 2, 2, 2>(a, s);
+    default: return launch_tile<T, 2, 4, 4, 2, 2>(a, s);
+    }
 }
 
 }  // namespace
+
+void gemm_mxfp4_tile(int E, int R, int N, int K, bool grouped, int& bm, int& bn)
+{
+    const Choice& c = kChoices[choose(E, R, N, K, grouped)];
+    bm = c.bm;
+    bn = c.bn;
+}
 
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s)
 {

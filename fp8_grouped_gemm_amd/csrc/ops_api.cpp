@@ -129,6 +129,15 @@ moe::MxQuantArgs mx_args(int32_t rows, int32_t cols, int32_t dtype, const void* 
     return a;
 }
 
+int check_gemm(int32_t groups, int32_t rows, int32_t n, int32_t k)
+{
+    if (groups < 1 || rows < 0 || n < 0 || k < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (k % 32 != 0 || k > (1 << 20) || groups > 1024 || rows >= (1 << 28) || n >= (1 << 28))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -263,10 +272,11 @@ int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
                    void* stream)
 {
     const int es = elem_bytes(dtype);
-    if (groups < 1 || rows < 0 || n < 0 || k < 1 || es < 2 || (!offsets && (groups != 1 || counts)))
+    if (es < 2 || (!offsets && (groups != 1 || counts)))
         return MOE_ERR_INVALID_ARG;
-    if (k % 32 != 0 || k > (1 << 20) || groups > 1024 || rows >= (1 << 28) || n >= (1 << 28))
-        return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int sizes = check_gemm(groups, rows, n, k);
+    if (sizes != MOE_OK)
+        return sizes;
     if (rows == 0 || n == 0)
         return MOE_OK;
     const int64_t ld = stride(y_ld, n);
@@ -290,6 +300,17 @@ int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
     g.y = static_cast<char*>(y);
     g.y_ld = ld * es;
     return launched(moe::launch_gemm_mxfp4(g, static_cast<hipStream_t>(stream)));
+}
+
+int moe_gemm_mxfp4_info(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t* tile_m,
+                        int32_t* tile_n)
+{
+    if (!tile_m || !tile_n || groups < 0)
+        return MOE_ERR_INVALID_ARG;
+    const int rc = check_gemm(groups == 0 ? 1 : groups, rows, n, k);
+    if (rc == MOE_OK)
+        moe::gemm_mxfp4_tile(groups == 0 ? 1 : groups, rows, n, k, groups != 0, *tile_m, *tile_n);
+    return rc;
 }
 
 }  // extern "C"

@@ -51,6 +51,8 @@ hipError_t launch_unpermute_bwd(const RowsArgs& a, hipStream_t s);
 hipError_t launch_quantize_mxfp4(const MxQuantArgs& a, hipStream_t s);
 hipError_t launch_dequantize_mxfp4(const MxQuantArgs& a, hipStream_t s);
 hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
+// Tile of a call (host only): only E, R, N, K and whether it is grouped count.
+void gemm_mxfp4_tile(int E, int R, int N, int K, bool grouped, int& bm, int& bn);
 
 // MOE_OK if the current device is gfx950 (moe_api.cpp).
 int device_status();

@@ -21,7 +21,7 @@ MOE_DTYPE_U8 = 3
 
 EXPORTED_SYMBOLS = (
     "moe_permute", "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd",
-    "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4",
+    "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4", "moe_gemm_mxfp4_info",
 )
 
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
@@ -45,6 +45,7 @@ def ops_lib():
         L.moe_quantize_mxfp4.argtypes = [i32] * 3 + [vp, i64, vp, vp, vp]
         L.moe_dequantize_mxfp4.argtypes = [i32] * 3 + [vp, vp, vp, i64, vp]
         L.moe_gemm_mxfp4.argtypes = [i32] * 5 + [vp] * 7 + [i64, vp]
+        L.moe_gemm_mxfp4_info.argtypes = [i32] * 4 + [vp] * 2
         for name in EXPORTED_SYMBOLS:
             getattr(L, name).restype = ctypes.c_int
         _ops = L
@@ -289,3 +290,12 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
         None if counts is None else _dense(counts, "counts", dev, i32, E),
         out.data_ptr(), _rows(out, "out", dev, dtype, R, N), _raw_stream(dev)), "moe_gemm_mxfp4")
     return out
+
+
+def moe_gemm_mxfp4_info(rows, n, k, groups=0):
+    """Rows and columns of y per workgroup in a moe_gemm_mxfp4 call of these
+    sizes (groups 0: dense), as {"tile_m", "tile_n"}."""
+    m, w = ctypes.c_int32(), ctypes.c_int32()
+    _check(ops_lib().moe_gemm_mxfp4_info(groups, rows, n, k, ctypes.addressof(m),
+                                         ctypes.addressof(w)), "moe_gemm_mxfp4_info")
+    return {"tile_m": m.value, "tile_n": w.value}

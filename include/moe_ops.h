@@ -132,12 +132,19 @@ int moe_dequantize_mxfp4(int32_t rows, int32_t cols, int32_t dtype, const uint8_
  * Scale code 0xFF on a block makes the sums it enters NaN.  a and b 16-byte
  * aligned.  y must not overlap an input.  Products and block sums are exact
  * in the matrix instruction up to f32 rounding of its result; K is summed in
- * an order that depends on the tile a call takes.
+ * an order that depends on the tile a call takes (moe_gemm_mxfp4_info): of
+ * calls with the same sizes, equal rows give equal bits.
  */
 int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t dtype,
                    const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
                    const int32_t* offsets, const int32_t* counts, void* y, int64_t y_ld,
                    void* stream);
+
+/* Tile a moe_gemm_mxfp4 call of these sizes takes (host only): the rows and
+ * columns of y per workgroup.  groups 0: dense; else that many segments.
+ * Ranges as for moe_gemm_mxfp4; MOE_ERR_INVALID_ARG also for a null output. */
+int moe_gemm_mxfp4_info(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t* tile_m,
+                        int32_t* tile_n);
 
 #ifdef __cplusplus
 }

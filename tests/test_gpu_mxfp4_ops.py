@@ -165,6 +165,55 @@ def test_dense_product(m, n, k):
     assert torch.equal(again, moe.moe_gemm_mxfp4(*d, dtype=torch.float32))
 
 
+# Ragged sizes of every tile: rows, n, k, segments (0: dense), the tile
+BY_TILE = [(11, 700, 1184, 0, (16, 16)), (29, 3000, 1056, 0, (32, 16)), (130, 1500, 2080, 0, (32, 64)),
+           (300, 8190, 1024, 0, (32, 128)), (511, 3000, 2144, 0, (64, 128)), (2047, 2100, 800, 0, (128, 128)),
+           (12001, 1001, 992, 0, (256, 256)), (45, 2050, 480, 20, (32, 64)), (333, 4000, 1056, 40, (32, 128)),
+           (2100, 600, 512, 20, (64, 128)), (6100, 1900, 544, 30, (128, 128)), (12300, 1000, 1024, 7, (256, 256))]
+
+
+@pytest.mark.parametrize("rows,n,k,groups,tile", BY_TILE, ids=str)
+def test_product_by_tile(rows, n, k, groups, tile):
+    say(f"product {rows} x {n} x {k}, {groups} segments: tile {tile}")
+    assert tuple(moe.moe_gemm_mxfp4_info(rows, n, k, groups).values()) == tile
+    rng = np.random.default_rng(rows)
+    E = max(1, groups)
+    a, asf = operand(rng, rows, k, 3)
+    b, bsf = operand(rng, E * n, k, 3)
+    table = torch.from_numpy(ou.E2M1).cuda()
+
+    def on_gpu(codes, sf):
+        v = torch.stack([table[(codes & 15).long()], table[(codes >> 4).long()]], -1).flatten(-2)
+        return v * torch.exp2(sf.double() - 127).repeat_interleave(32, -1)
+
+    d = [torch.from_numpy(v).cuda() for v in (a, asf, b, bsf)]
+    va, vb = on_gpu(*d[:2]), on_gpu(*d[2:]).view(E, n, k)
+    args, lens = d, [rows]
+    kw = {}
+    if groups:
+        lens = rng.multinomial(rows, rng.dirichlet(np.full(E, 2.0)))
+        lens[E // 2] += lens[0]
+        lens[0] = 0                                         # an expert without rows
+        off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        kw = dict(offsets=torch.from_numpy(off).cuda())
+        args = [d[0], d[1], d[2].view(E, n, -1), d[3].view(E, n, -1)]
+    for dtype in (torch.bfloat16, torch.float32):
+        y = torch.full((rows, n), 5.0, dtype=dtype, device="cuda")
+        moe.moe_gemm_mxfp4(*args, out=y, **kw)
+        first = 0
+        for e, c in enumerate(lens):
+            if c:
+                s = slice(first, first + int(c))
+                ex, mag = va[s] @ vb[e].t(), va[s].abs() @ vb[e].abs().t()
+                inner = (k / 64 + 1 + 8) * 2.0 ** -22 * mag
+                off_by = (y[s].double() - ex).abs()
+                lim = inner + ou.half_step(dtype) * (ex.abs() + inner) + ou.least(dtype)
+                assert torch.all(off_by <= lim), (e, (off_by / lim).max().item())
+            first += int(c)
+    z = torch.full_like(y, 5.0)
+    assert torch.equal(moe.moe_gemm_mxfp4(*args, out=z, **kw), y)
+
+
 @pytest.mark.parametrize("spread", [8, 31])
 @pytest.mark.parametrize("m,n,k", [(4, 40, 512), (40, 40, 512), (130, 140, 512), (700, 300, 512)])
 def test_product_of_far_scales(m, n, k, spread):

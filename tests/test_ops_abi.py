@@ -124,3 +124,28 @@ def test_binding_refuses_host_tensors():
               lambda: moe.moe_gemm_mxfp4(u, u[:, :1], u, u[:, :1])):
         with pytest.raises(ValueError, match="expected a GPU"):
             f()
+
+
+TILES = [(16, 16), (32, 16), (32, 64), (32, 128), (64, 128), (128, 128), (256, 256)]
+
+
+def test_product_tiles():
+    info = lambda *a: tuple(moe.moe_gemm_mxfp4_info(*a).values())
+    # measured points of the rule: the best or within 10 % of it
+    for sizes, tile in (((1, 4096, 7168), 0), ((32, 4096, 4096), 1), ((128, 4096, 7168), 2),
+                        ((512, 4096, 4096), 4), ((2048, 4096, 4096), 5), ((4096, 4096, 4096), 6),
+                        ((32, 4096, 4096, 32), 3), ((768, 4096, 4096, 32), 3),
+                        ((6144, 4096, 4096, 32), 5), ((12288, 4096, 4096, 32), 6)):
+        assert info(*sizes) == TILES[tile], sizes
+    # every size has a tile
+    for rows in (0, 1, 7, 300, 1 << 27):
+        for n in (0, 1, 4097, 1 << 27):
+            for g in (0, 1, 1024):
+                assert info(rows, n, 32, g) in TILES
+    for bad, code in (((-1, 4, 32), INV), ((4, 4, 0), INV), ((4, 4, 48), SHAPE), ((4, 4, 32, -1), INV),
+                      ((4, 4, 32, 1025), SHAPE)):
+        with pytest.raises(moe.MoEError) as e:
+            info(*bad)
+        assert e.value.code == code
+    m = ctypes.c_int32()
+    assert ops.ops_lib().moe_gemm_mxfp4_info(0, 4, 4, 32, None, ctypes.addressof(m)) == INV
