@@ -7,7 +7,8 @@
 //   unpermute      y[t] = sum_j w[tK + j] yp[src_row[tK + j]]
 //   its gradients  dyp[src_row[f]] = w[f] dy[f / K],  dw[f] = dy[f / K] . yp[src_row[f]]
 //
-// All four move bytes and compute next to nothing, so HBM bounds them.  They
+// All four move bytes and compute next to nothing, so HBM bounds them (4.9 to
+// 6.0 TB/s at 8192 x 6 x 7168 and 4096 x 8 x 4096; a large copy reaches 5.2).  They
 // walk the token side, not the pool: a token's row is read once (or its
 // sums stay in registers) and its K pool rows are written or read whole,
 // where walking the pool would read every token row K times.  Nothing is
@@ -27,6 +28,7 @@ constexpr int kPadRows = 4;  // pool rows each wave looks over for padding
 
 // Zeros the padding rows (row_src outside [0, TK)) among pool rows
 // [r0, r0 + kPadRows) below `used`, by one wave.
+template <bool NT>
 __device__ __forceinline__ void clear_padding(const RowsArgs& a, int r0, int row_bytes, int lane)
 {
     const int used = a.used ? min(*a.used, a.R) : a.R;
@@ -39,10 +41,26 @@ __device__ __forceinline__ void clear_padding(const RowsArgs& a, int r0, int row
         char* p = a.pool_out + (int64_t)r * a.pool_out_ld;
         int at = lane * 16;
         for (; at + 16 <= row_bytes; at += 64 * 16)
-            store16(p + at, zero);
+            store16<NT>(p + at, zero);
         for (; at < row_bytes; ++at)  // the one lane (if any) holding the ragged end
             p[at] = 0;
     }
+}
+
+// Whether a call's pool rows stream past the caches (nontemporal accesses):
+// whole aligned 16-byte pieces, and more of them than the eight L2s hold
+// twice over.  Measured cached and streamed, us: permute 8192 x 6 x 7168 bf16
+// 175 and 145, its gradient 4096 x 8 x 4096 f32 109 and 92, unpermute 173 and
+// 161, its gradient 4096 x 8 x 4096 117 and 110; but rows of 4097 bf16
+// (unaligned) 52 and 57, the gradient at 512 x 8 x 4096 (34 MB) 15 and 19.  The
+// token rows stay cached: several workgroups read them (permute 145, 176
+// streamed).
+bool streams(const RowsArgs& a, const void* pool, int64_t pool_ld, int size)
+{
+    const int64_t row = (int64_t)a.width * size;
+    const uintptr_t tok = reinterpret_cast<uintptr_t>(a.tok ? a.tok : a.tok_out);
+    return (int64_t)a.T * a.K * row > (INT64_C(64) << 20) &&
+           (row | pool_ld | a.tok_ld | (int64_t)reinterpret_cast<uintptr_t>(pool) | (int64_t)tok) % 16 == 0;
 }
 
 // Workgroups of one launch: token_wgs over tokens, then those that look for
@@ -68,12 +86,13 @@ int row_threads(int64_t n)
 // x row -> its K pool rows, one 16-byte piece per thread.  A row's last piece
 // reaches back to stay whole (it writes bytes the previous piece also
 // writes, with the same values); rows under 16 bytes go byte by byte.
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void permute_rows(RowsArgs a, int row_bytes, int tpr,
                                                          int pieces, unsigned token_wgs)
 {
     if (blockIdx.x >= token_wgs) {
         const int wave = (blockIdx.x - token_wgs) * (kThreads / 64) + (threadIdx.x >> 6);
-        clear_padding(a, wave * kPadRows, row_bytes, threadIdx.x & 63);
+        clear_padding<NT>(a, wave * kPadRows, row_bytes, threadIdx.x & 63);
         return;
     }
     const unsigned g = blockIdx.x / pieces;
@@ -97,13 +116,14 @@ __global__ __launch_bounds__(kThreads) void permute_rows(RowsArgs a, int row_byt
     for (int j = 0; j < a.K; ++j) {
         const int r = slot[j];
         if (r >= 0 && r < a.R)
-            store16(a.pool_out + (int64_t)r * a.pool_out_ld + at, v);
+            store16<NT>(a.pool_out + (int64_t)r * a.pool_out_ld + at, v);
     }
 }
 
 // out[t] = sum_j w[tK + j] pool[src_row[tK + j]], j ascending, one vector of the row
-// per thread; four slots' loads are in flight at a time.
-template <class E, bool W>
+// per thread; four slots' loads are in flight at a time (eight: 213 us for 161 at
+// 8192 x 6 x 7168, their registers halve the waves; two: 162).
+template <class E, bool W, bool NT>
 __global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int pieces)
 {
     const unsigned g = blockIdx.x / pieces;
@@ -118,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int 
 #pragma unroll
     for (int i = 0; i < E::VEC; ++i)
         acc[i] = 0.f;
-    constexpr int U = 4;
+        constexpr int U = 4;
     for (int j0 = 0; j0 < a.K; j0 += U) {
         float v[U][E::VEC], wt[U];
         bool on[U];
@@ -130,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int 
             if (on[u]) {
                 if (W)
                     wt[u] = w[j0 + u];
-                load_vec<E>(a.pool + (int64_t)r * a.pool_ld + (int64_t)c * E::SIZE, n, v[u]);
+                load_vec<E, NT>(a.pool + (int64_t)r * a.pool_ld + (int64_t)c * E::SIZE, n, v[u]);
             }
         }
 #pragma unroll
@@ -140,20 +160,20 @@ __global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int 
                 for (int i = 0; i < E::VEC; ++i)
                     acc[i] = W ? __builtin_fmaf(wt[u], v[u][i], acc[i]) : acc[i] + v[u][i];
     }
-    store_vec<E>(a.tok_out + (int64_t)t * a.tok_ld + (int64_t)c * E::SIZE, n, acc);
+    store_vec<E, NT>(a.tok_out + (int64_t)t * a.tok_ld + (int64_t)c * E::SIZE, n, acc);
 }
 
 // dyp row and dw of one slot per wave: the lanes stride over the row, write
 // w dy and sum dy yp, and the wave's 64 sums meet in a butterfly (a fixed
 // order).  Consecutive waves take consecutive slots, so the K waves of a
 // token read its dy row together.
-template <class E, bool DYP, bool DW>
+template <class E, bool DYP, bool DW, bool NT>
 __global__ __launch_bounds__(kThreads) void unpermute_grad(RowsArgs a, unsigned token_wgs)
 {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x >= token_wgs) {
-        clear_padding(a, ((blockIdx.x - token_wgs) * (kThreads / 64) + wave) * kPadRows,
+        clear_padding<NT>(a, ((blockIdx.x - token_wgs) * (kThreads / 64) + wave) * kPadRows,
                       a.width * E::SIZE, lane);
         return;
     }
@@ -177,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_grad(RowsArgs a, unsigned 
         float d[E::VEC], y[E::VEC];
         load_vec<E>(dy + (int64_t)c * E::SIZE, n, d);
         if (DW) {
-            load_vec<E>(yp + (int64_t)c * E::SIZE, n, y);
+            load_vec<E, NT>(yp + (int64_t)c * E::SIZE, n, y);
 #pragma unroll
             for (int i = 0; i < E::VEC; ++i)
                 sum = __builtin_fmaf(d[i], y[i], sum);
@@ -186,7 +206,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_grad(RowsArgs a, unsigned 
 #pragma unroll
             for (int i = 0; i < E::VEC; ++i)
                 d[i] *= w;
-            store_vec<E>(dyp + (int64_t)c * E::SIZE, n, d);
+            store_vec<E, NT>(dyp + (int64_t)c * E::SIZE, n, d);
         }
     }
     if (DW) {
@@ -213,8 +233,9 @@ hipError_t launch_permute(const RowsArgs& a, hipStream_t s)
         return hipErrorInvalidValue;
     if (wgs + pad == 0)
         return hipSuccess;
-    hipLaunchKernelGGL(permute_rows, dim3((unsigned)wgs + pad), dim3(kThreads), 0, s, a, row_bytes,
-                       tpr, pieces, (unsigned)wgs);
+    const auto kernel = streams(a, a.pool_out, a.pool_out_ld, size) ? permute_rows<true> : permute_rows<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs + pad), dim3(kThreads), 0, s, a, row_bytes, tpr, pieces,
+                       (unsigned)wgs);
     return hipGetLastError();
 }
 
@@ -227,10 +248,10 @@ static hipError_t launch_token_sums(const RowsArgs& a, hipStream_t s)
     const int64_t wgs = (int64_t)((a.T + per - 1) / per) * pieces;
     if (wgs >= (INT64_C(1) << 31))
         return hipErrorInvalidValue;
-    if (a.w)
-        hipLaunchKernelGGL((token_sums<E, true>), dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
-    else
-        hipLaunchKernelGGL((token_sums<E, false>), dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
+    const bool nt = streams(a, a.pool, a.pool_ld, E::SIZE);
+    const auto kernel = a.w ? (nt ? token_sums<E, true, true> : token_sums<E, true, false>)
+                            : (nt ? token_sums<E, false, true> : token_sums<E, false, false>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
     return hipGetLastError();
 }
 
@@ -252,12 +273,17 @@ static hipError_t launch_grad(const RowsArgs& a, hipStream_t s)
     const dim3 grid(wgs + pad), block(kThreads);
     if (wgs + pad == 0)
         return hipSuccess;
-    if (a.pool_out && a.dw)
-        hipLaunchKernelGGL((unpermute_grad<E, true, true>), grid, block, 0, s, a, wgs);
-    else if (a.pool_out)
-        hipLaunchKernelGGL((unpermute_grad<E, true, false>), grid, block, 0, s, a, wgs);
-    else
-        hipLaunchKernelGGL((unpermute_grad<E, false, true>), grid, block, 0, s, a, wgs);
+    bool nt = true;
+    if (a.dw)
+        nt = nt && streams(a, a.pool, a.pool_ld, E::SIZE);
+    if (a.pool_out)
+        nt = nt && streams(a, a.pool_out, a.pool_out_ld, E::SIZE);
+    auto kernel = nt ? unpermute_grad<E, true, true, true> : unpermute_grad<E, true, true, false>;
+    if (!a.dw)
+        kernel = nt ? unpermute_grad<E, true, false, true> : unpermute_grad<E, true, false, false>;
+    else if (!a.pool_out)
+        kernel = nt ? unpermute_grad<E, false, true, true> : unpermute_grad<E, false, true, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, wgs);
     return hipGetLastError();
 }
 

@@ -9,18 +9,23 @@ typedef unsigned int rows_u32x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes at any byte address: gfx950 global accesses need no alignment, so
 // rows of odd width take the same wide accesses as aligned ones.
-struct __attribute__((packed, aligned(1))) Bytes16 {
-    rows_u32x4 v;
-};
+typedef unsigned int bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
+template <bool NT = false>
 __device__ __forceinline__ rows_u32x4 load16(const char* p)
 {
-    return reinterpret_cast<const Bytes16*>(p)->v;
+    if constexpr (NT)
+        return __builtin_nontemporal_load(reinterpret_cast<const bytes16*>(p));
+    return *reinterpret_cast<const bytes16*>(p);
 }
 
+template <bool NT = false>
 __device__ __forceinline__ void store16(char* p, rows_u32x4 v)
 {
-    reinterpret_cast<Bytes16*>(p)->v = v;
+    if constexpr (NT)
+        __builtin_nontemporal_store((bytes16)v, reinterpret_cast<bytes16*>(p));
+    else
+        *reinterpret_cast<bytes16*>(p) = v;
 }
 
 // An element type: its size, how many fit 16 bytes, and the conversions
@@ -116,11 +121,11 @@ struct F32 {
 };
 
 // The n <= VEC elements of one vector at p (n < VEC: a row's last ones).
-template <class T>
+template <class T, bool NT = false>
 __device__ __forceinline__ void load_vec(const char* p, int n, float* f)
 {
     if (n >= T::VEC) {
-        T::unpack(load16(p), f);
+        T::unpack(load16<NT>(p), f);
     } else {
 #pragma unroll
         for (int i = 0; i < T::VEC; ++i)
@@ -128,11 +133,11 @@ __device__ __forceinline__ void load_vec(const char* p, int n, float* f)
     }
 }
 
-template <class T>
+template <class T, bool NT = false>
 __device__ __forceinline__ void store_vec(char* p, int n, const float* f)
 {
     if (n >= T::VEC) {
-        store16(p, T::pack(f));
+        store16<NT>(p, T::pack(f));
     } else {
 #pragma unroll
         for (int i = 0; i < T::VEC; ++i)
