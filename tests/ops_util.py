@@ -89,7 +89,7 @@ def unpermute_grads(dy, yp, lists, w, before):
 def quantised(x):
     """(values in units of the block scale, scale exponents) of float64 rows by the definition:
     the smallest power of two >= max(amax, 1e-10) / 6, nearest e2m1 value, ties to the even code."""
-    blk = x.reshape(x.shape[0], -1, 32)
+    blk = x.reshape(x.shape[0], x.shape[1] // 32, 32)
     # 1e-10 as the float32 the rule uses; amax <= 6 * 2^e compared exactly
     amax = np.maximum(abs(blk).max(-1), float(np.float32(1e-10)))
     e = np.floor(np.log2(amax)).astype(np.int64) - 4
