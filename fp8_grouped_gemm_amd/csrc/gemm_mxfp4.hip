@@ -511,6 +511,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
     constexpr int PIECES = NI * 32 / T::VEC;  // 16-byte pieces of a row
     constexpr int PER = 64 / PIECES;          // rows per store instruction
     const int c = col0 + wn * NI * 32 + (lane % PIECES) * T::VEC;
+    // whole aligned pieces bypass the caches: y is not read here, and what a
+    // tile shares in its L2 stays (2048 x 4096 x 4096: 26.6 us cached, 25.1;
+    // 8192 x 8192 x 7168: 278, 273; unaligned ones would be split)
+    const bool nt = (reinterpret_cast<uintptr_t>(a.y) | a.y_ld) % 16 == 0;
 #pragma unroll
     for (int m = 0; m < MI; ++m) {
 #pragma unroll
@@ -529,8 +533,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
             const char* src = reinterpret_cast<const char*>(out) + lrow * C::OUT_LD + (lane % PIECES) * 16;
             if (r < t.rows && c < a.N) {
                 char* dst = a.y + (int64_t)(t.row0 + r) * a.y_ld + (int64_t)c * T::SIZE;
+                const rows_u32x4 v = *reinterpret_cast<const rows_u32x4*>(src);
                 if (c + T::VEC <= a.N) {
-                    store16(dst, *reinterpret_cast<const rows_u32x4*>(src));
+                    if (nt)
+                        store16<true>(dst, v);
+                    else
+                        store16(dst, v);
                 } else {
                     for (int i = 0; i < a.N - c; ++i)
                         T::store(dst + i * T::SIZE, T::load(src + i * T::SIZE));
