@@ -299,15 +299,23 @@ struct TileCfg {
     static_assert(SMEM <= 160 * 1024 && W * 32 * OUT_LD <= SMEM, "LDS");
 };
 
-// 16 bytes per lane from byte `off` of the resource to LDS at lds + 16 * lane.
+// 16 bytes per lane from byte `off` of the resource to LDS at lds + 16 * lane
+// (NT: nontemporal).
+template <bool NT>
 __device__ __forceinline__ void dma16_rsrc(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r),
-                 "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory", "m0");
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds);
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(r), "s"(at)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(at)
+                     : "memory", "m0");
 }
 
-template <class T, int WM, int WN, int MI, int NI, int NBUF>
+// ONCE: b is large and a row tile covers a segment, so b streams past the
+// caches (streams_b).
+template <class T, int WM, int WN, int MI, int NI, int NBUF, bool ONCE>
 __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col_tiles)
 {
     using C = TileCfg<T, WM, WN, MI, NI, NBUF>;
@@ -337,8 +345,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
     auto copy = [&](int st, int buf, int q) {
         constexpr int QA = BM / 8 / W;  // copies of a's rows
         const uint32_t at = off0 + (q < QA ? q : q - QA) * (8 * W) * pitch + st * 128;
-        dma16_rsrc(q < QA ? ra : rb, st * 8 + chunk < nb ? at : kOutside,
-                   lds0 + buf * C::STAGE + q * W * 1024);
+        const uint32_t src = st * 8 + chunk < nb ? at : kOutside, dst = lds0 + buf * C::STAGE + q * W * 1024;
+        if (q < QA)
+            dma16_rsrc<false>(ra, src, dst);
+        else
+            dma16_rsrc<ONCE>(rb, src, dst);
     };
     // Scale codes: thread i takes rows i, i + TH, ... of the ROWS.
     auto code_row = [&](int row) {  // rows past the tile repeat its last
@@ -576,7 +587,7 @@ hipError_t launch_few(const MxGemmArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <class T, int WM, int WN, int MI, int NI, int NBUF>
+template <class T, int WM, int WN, int MI, int NI, int NBUF, bool ONCE = false>
 hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
 {
     using C = TileCfg<T, WM, WN, MI, NI, NBUF>;
@@ -584,7 +595,7 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
     const unsigned grid = tile_grid(a, C::BM, ct);
     if (!grid)
         return hipErrorInvalidValue;
-    auto kernel = mxfp4_tile<T, WM, WN, MI, NI, NBUF>;
+    auto kernel = mxfp4_tile<T, WM, WN, MI, NI, NBUF, ONCE>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != hipSuccess)
@@ -617,7 +628,7 @@ struct Choice {
 };
 constexpr Choice kChoices[] = {
     {16, 16, 2, 2.0, 0.22, 2.0, 0.12},  {32, 16, 2, 2.0, 0.31, 2.0, 0.16},
-    {32, 64, 2, 1.5, 0.40, 1.5, 0.28},  {32, 128, 3, 3.0, 0.83, 2.0, 0.40},
+    {32, 64, 2, 1.5, 0.40, 1.5, 0.28},  {32, 128, 3, 3.0, 0.95, 2.0, 0.40},
     {64, 128, 1, 2.5, 0.47, 2.5, 0.36}, {128, 128, 2, 5.0, 1.30, 4.0, 0.75},
     {256, 256, 1, 6.0, 2.10, 6.0, 2.10},
 };
@@ -652,15 +663,28 @@ int choose(int E, int R, int N, int K, bool grouped)
     return best;
 }
 
+// Whether the tiles of bm rows read b (nearly) once, and more of it than the
+// L2s hold twice over: its copies are then nontemporal.  Measured cached and
+// not, us: 768 rows over 32 experts of 4096 x 4096 63.7 and 62.0, 600 rows 65.1
+// and 61.7, 64 rows 47.9 and 44.4, 768 rows over 64 experts of 2048 x 4096 68.0 and
+// 63.9; but dense, where row tiles share b, 512 rows 11.6 and 12.6, 2048 rows 26.1
+// and 28.2.
+bool streams_b(const MxGemmArgs& a, int bm)
+{
+    return (int64_t)a.E * a.N * (a.K / 2) > (INT64_C(64) << 20) && a.R <= (int64_t)a.E * bm;
+}
+
 template <class T>
 hipError_t launch(const MxGemmArgs& a, hipStream_t s)
 {
-    switch (choose(a.E, a.R, a.N, a.K, a.offsets != nullptr)) {
+    const int choice = choose(a.E, a.R, a.N, a.K, a.offsets != nullptr);
+    const bool once = streams_b(a, kChoices[choice].bm);
+    switch (choice) {
     case 0: return launch_few<T, 1, 1, 8, 2>(a, s);
     case 1: return launch_few<T, 2, 1, 8, 2>(a, s);
-    case 2: return launch_tile<T, 1, 2, 1, 1, 4>(a, s);
-    case 3: return launch_tile<T, 1, 4, 1, 1, 2>(a, s);
-    case 4: return launch_tile<T, 2, 4, 1, 1, 3>(a, s);
+    case 2: return once ? launch_tile<T, 1, 2, 1, 1, 4, true>(a, s) : launch_tile<T, 1, 2, 1, 1, 4>(a, s);
+    case 3: return once ? launch_tile<T, 1, 4, 1, 1, 2, true>(a, s) : launch_tile<T, 1, 4, 1, 1, 2>(a, s);
+    case 4: return once ? launch_tile<T, 2, 4, 1, 1, 3, true>(a, s) : launch_tile<T, 2, 4, 1, 1, 3>(a, s);
     case 5: return launch_tile<T, 2, 2, 2, 2, 2>(a, s);
     default: return launch_tile<T, 2, 4, 4, 2, 2>(a, s);
     }
