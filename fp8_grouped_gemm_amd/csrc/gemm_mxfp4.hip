@@ -370,18 +370,21 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
                     for (int j = 0; j < 4; ++j)
                         codes[q][4 * i + j] = u.v[j];
                 }
-            } else {  // the group K ends in, byte by byte
-                const int last = nb - 1 - g * 8 * kCodeStages;
-#pragma unroll
-                for (int i = 0; i < 2 * kCodeStages; ++i) {
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t c = p[max(0, min(4 * i + j, last))];
-                        w |= (4 * i + j <= last ? c : 127u) << (8 * j);
-                    }
-                    codes[q][i] = w;
+            } else {  // the group K ends in: n codes, whole words and a last part
+                struct __attribute__((packed, aligned(1))) U1 { uint32_t v; };
+                const int n = nb - g * 8 * kCodeStages, part = n % 4;
+                uint32_t end = 0;
+                if (part && nb >= 4) {  // the row's last four codes, those before the part shifted out
+                    end = reinterpret_cast<const U1*>(p + n - 4)->v >> (8 * (4 - part));
+                } else {
+                    for (int j = 0; j < part; ++j)
+                        end |= (uint32_t)p[n - part + j] << (8 * j);
                 }
+                end |= 0x7F7F7F7Fu << (8 * part);
+#pragma unroll
+                for (int i = 0; i < 2 * kCodeStages; ++i)
+                    codes[q][i] = 4 * i + 4 <= n ? reinterpret_cast<const U1*>(p + 4 * i)->v
+                                                 : i == n / 4 ? end : 0x7F7F7F7Fu;
             }
         }
     };
@@ -571,7 +574,7 @@ unsigned tile_grid(const MxGemmArgs& a, int bm, int col_tiles)
 {
     int64_t rt = (a.R + bm - 1) / bm;
     if (a.offsets)
-        rt = std::min<int64_t>(a.R, a.R / bm + a.E);
+        rt = std::min<int64_t>(a.slots, a.slots / bm + a.E);
     const int64_t g = (rt * col_tiles + 7) / 8 * 8;
     return g < (INT64_C(1) << 31) ? (unsigned)g : 0u;
 }
@@ -671,13 +674,13 @@ int choose(int E, int R, int N, int K, bool grouped)
 // and 28.2.
 bool streams_b(const MxGemmArgs& a, int bm)
 {
-    return (int64_t)a.E * a.N * (a.K / 2) > (INT64_C(64) << 20) && a.R <= (int64_t)a.E * bm;
+    return (int64_t)a.E * a.N * (a.K / 2) > (INT64_C(64) << 20) && a.slots <= (int64_t)a.E * bm;
 }
 
 template <class T>
 hipError_t launch(const MxGemmArgs& a, hipStream_t s)
 {
-    const int choice = choose(a.E, a.R, a.N, a.K, a.offsets != nullptr);
+    const int choice = choose(a.E, a.slots, a.N, a.K, a.offsets != nullptr);
     const bool once = streams_b(a, kChoices[choice].bm);
     switch (choice) {
     case 0: return launch_few<T, 1, 1, 8, 2>(a, s);

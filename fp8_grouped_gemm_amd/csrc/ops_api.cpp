@@ -268,11 +268,11 @@ int moe_dequantize_mxfp4(int32_t rows, int32_t cols, int32_t dtype, const uint8_
 
 int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t dtype,
                    const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
-                   const int32_t* offsets, const int32_t* counts, void* y, int64_t y_ld,
-                   void* stream)
+                   const int32_t* offsets, const int32_t* counts, int32_t slots, void* y,
+                   int64_t y_ld, void* stream)
 {
     const int es = elem_bytes(dtype);
-    if (es < 2 || (!offsets && (groups != 1 || counts)))
+    if (es < 2 || slots < 0 || (!offsets && (groups != 1 || counts)))
         return MOE_ERR_INVALID_ARG;
     const int sizes = check_gemm(groups, rows, n, k);
     if (sizes != MOE_OK)
@@ -295,6 +295,7 @@ int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
         return rc;
     moe::MxGemmArgs g{};
     g.E = groups; g.R = rows; g.N = n; g.K = k; g.dtype = dtype;
+    g.slots = offsets && slots > 0 && slots < rows ? slots : rows;
     g.a = a; g.a_sf = a_sf; g.b = b; g.b_sf = b_sf;
     g.offsets = offsets; g.counts = counts;
     g.y = static_cast<char*>(y);

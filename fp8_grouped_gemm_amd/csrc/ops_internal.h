@@ -34,6 +34,7 @@ struct MxQuantArgs {
 
 struct MxGemmArgs {
     int32_t E, R, N, K;
+    int32_t slots;             // most rows of all segments together (dense: R)
     int32_t dtype;
     const uint8_t* a;
     const uint8_t* a_sf;

@@ -44,7 +44,7 @@ def ops_lib():
                                                     vp]
         L.moe_quantize_mxfp4.argtypes = [i32] * 3 + [vp, i64, vp, vp, vp]
         L.moe_dequantize_mxfp4.argtypes = [i32] * 3 + [vp, vp, vp, i64, vp]
-        L.moe_gemm_mxfp4.argtypes = [i32] * 5 + [vp] * 7 + [i64, vp]
+        L.moe_gemm_mxfp4.argtypes = [i32] * 5 + [vp] * 6 + [i32, vp, i64, vp]
         L.moe_gemm_mxfp4_info.argtypes = [i32] * 4 + [vp] * 2
         for name in EXPORTED_SYMBOLS:
             getattr(L, name).restype = ctypes.c_int
@@ -258,15 +258,17 @@ def moe_dequantize_mxfp4(codes, sf, dtype=torch.bfloat16, out=None, stream=None)
 
 
 def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=None,
-                   stream=None):
+                   slots=0, stream=None):
     """y [R, N] = a b^T of 4-bit microscaled a [R, K/2], a_sf [R, K/32] and
     b [N, K/2], b_sf [N, K/32] (dense), or b [E, N, K/2], b_sf [E, N, K/32]
     with offsets int32 [E+1] and counts int32 [E] (None: the segments'
     whole lengths): expert e's rows offsets[e] .. + counts[e], the other rows
     of y left as they were (a new y: unset).  y's type: out's, else dtype,
-    else bf16."""
+    else bf16.  slots: an upper bound of the rows of all segments together
+    (T * K), where a pool with padding has more rows than that (0: R)."""
     if not _here(a, stream):
-        return _elsewhere(moe_gemm_mxfp4, a, stream, a, a_sf, b, b_sf, offsets, counts, dtype, out)
+        return _elsewhere(moe_gemm_mxfp4, a, stream, a, a_sf, b, b_sf, offsets, counts, dtype, out,
+                          slots)
     dev, u8, i32 = a.get_device(), torch.uint8, torch.int32
     if a.dim() != 2 or b.dim() != (2 if offsets is None else 3):
         raise ValueError(f"a: shape {tuple(a.shape)}, b: shape {tuple(b.shape)}, expected "
@@ -287,7 +289,7 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
         _dense(a_sf, "a_sf", dev, u8, (R, nb)), _dense(b, "b", dev, u8, lead + (N, k2)),
         _dense(b_sf, "b_sf", dev, u8, lead + (N, nb)),
         None if offsets is None else _dense(offsets, "offsets", dev, i32, E + 1),
-        None if counts is None else _dense(counts, "counts", dev, i32, E),
+        None if counts is None else _dense(counts, "counts", dev, i32, E), slots,
         out.data_ptr(), _rows(out, "out", dev, dtype, R, N), _raw_stream(dev)), "moe_gemm_mxfp4")
     return out
 

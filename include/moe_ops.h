@@ -127,7 +127,10 @@ int moe_dequantize_mxfp4(int32_t rows, int32_t cols, int32_t dtype, const uint8_
  * offsets[e] .. offsets[e] + counts[e] - 1 (counts NULL: up to
  * offsets[e + 1]), int32 device arrays as moe_route writes them; the rows of
  * y outside the segments (padding among them) are left as they were, and
- * a segment is cut at `rows`.  Segments do not overlap.
+ * a segment is cut at `rows`.  Segments do not overlap.  slots: an upper bound
+ * of the rows of all segments together (T*K of the routing), for calls whose
+ * `rows` counts a padded pool; it sizes the launch, so that rows beyond it may
+ * be left as they were.  0: rows.  Dense calls ignore it.
  * k % 32 == 0, 32 <= k <= 2^20, groups <= 1024, rows < 2^28, n < 2^28.
  * Scale code 0xFF on a block makes the sums it enters NaN.  a and b 16-byte
  * aligned.  y must not overlap an input.  Products and block sums are exact
@@ -137,12 +140,12 @@ int moe_dequantize_mxfp4(int32_t rows, int32_t cols, int32_t dtype, const uint8_
  */
 int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t dtype,
                    const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
-                   const int32_t* offsets, const int32_t* counts, void* y, int64_t y_ld,
-                   void* stream);
+                   const int32_t* offsets, const int32_t* counts, int32_t slots, void* y,
+                   int64_t y_ld, void* stream);
 
 /* Tile a moe_gemm_mxfp4 call of these sizes takes (host only): the rows and
- * columns of y per workgroup.  groups 0: dense; else that many segments.
- * Ranges as for moe_gemm_mxfp4; MOE_ERR_INVALID_ARG also for a null output. */
+ * columns of y per workgroup.  groups 0: dense; else that many segments, of
+ * `rows` rows in all (a call's slots, if it states them).  Ranges as for moe_gemm_mxfp4; MOE_ERR_INVALID_ARG also for a null output. */
 int moe_gemm_mxfp4_info(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t* tile_m,
                         int32_t* tile_n);
 

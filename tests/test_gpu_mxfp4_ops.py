@@ -256,6 +256,14 @@ def test_grouped_product(lens, n, k, align):
             s = slice(offsets[e], offsets[e] + c)
             if c:
                 check_product(y[s], *exact(a[s], asf[s], b[e], bsf[e]), k, dtype, (e, dtype))
+    for slots in (sum(lens), sum(lens) + 5):                # the launch sized by the rows there are
+        z = torch.full((rows, n), 55.0, dtype=torch.float32, device="cuda")
+        moe.moe_gemm_mxfp4(*d, counts=counts, out=z, slots=slots)
+        assert torch.all(z[torch.from_numpy(~live).cuda()] == 55)
+        for e, c in enumerate(lens):
+            s = slice(offsets[e], offsets[e] + c)
+            if c:
+                check_product(z[s], *exact(a[s], asf[s], b[e], bsf[e]), k, torch.float32, (e, slots))
     if align == 1:                                          # whole segments without counts
         z = torch.full_like(y, 55.0)
         assert torch.equal(moe.moe_gemm_mxfp4(*d, out=z), y)

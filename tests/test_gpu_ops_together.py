@@ -52,7 +52,7 @@ class Layer:
         codes, sf = moe.moe_quantize_mxfp4(self.x)
         xp = moe.moe_permute(codes, r["row_src"], r["src_row"], r["offsets"])
         xp_sf = moe.moe_permute(sf, r["row_src"], r["src_row"], r["offsets"])
-        seg = dict(offsets=r["offsets"], counts=r["counts"])
+        seg = dict(offsets=r["offsets"], counts=r["counts"], slots=T * K)
         gu = torch.zeros(xp.shape[0], 2 * I, dtype=torch.bfloat16, device="cuda")
         moe.moe_gemm_mxfp4(xp, xp_sf, self.w1, self.w1_sf, out=gu, **seg)
         g, u = gu.float().chunk(2, 1)

@@ -53,7 +53,7 @@ GRAD = dict(**ROWS, dy=X, dy_ld=0, yp=Y, yp_ld=0, row_src=Z, src_row=V, used=V +
 QUANT = dict(rows=4, cols=64, dtype=BF16, x=X, x_ld=0, codes=Y, sf=Z, stream=0)
 DEQUANT = dict(rows=4, cols=64, dtype=BF16, codes=Y, sf=Z, x=X, x_ld=0, stream=0)
 GEMM = dict(groups=2, rows=16, n=32, k=64, dtype=BF16, a=X, a_sf=Y, b=Z, b_sf=V,
-            offsets=V + 4096, counts=V + 8192, y=W, y_ld=0, stream=0)
+            offsets=V + 4096, counts=V + 8192, slots=0, y=W, y_ld=0, stream=0)
 
 BAD_ROWS = [(dict(T=-1), INV), (dict(K=0), INV), (dict(R=-1), INV), (dict(width=0), INV),
             (dict(dtype=4), INV), (dict(dtype=-1), INV), (dict(K=1025), SHAPE),
@@ -90,7 +90,7 @@ BAD_ROWS = [(dict(T=-1), INV), (dict(K=0), INV), (dict(R=-1), INV), (dict(width=
         (dict(codes=0), INV), (dict(sf=0), INV), (dict(x_ld=-64), INV), (dict(x=Y), INV)]),
     ("moe_gemm_mxfp4", GEMM, [
         (dict(groups=0), INV), (dict(rows=-1), INV), (dict(n=-1), INV), (dict(k=0), INV),
-        (dict(dtype=U8), INV), (dict(offsets=0), INV), (dict(offsets=0, groups=1), INV),
+        (dict(dtype=U8), INV), (dict(offsets=0), INV), (dict(offsets=0, groups=1), INV), (dict(slots=-1), INV),
         (dict(k=80), SHAPE), (dict(k=(1 << 20) + 32), SHAPE), (dict(groups=1025), SHAPE),
         (dict(rows=1 << 28), SHAPE), (dict(n=1 << 28), SHAPE), (dict(a=0), INV), (dict(b=0), INV),
         (dict(a_sf=0), INV), (dict(b_sf=0), INV), (dict(y=0), INV), (dict(a=X + 8), INV),
