@@ -313,8 +313,8 @@ __device__ __forceinline__ void dma16_rsrc(__amdgpu_buffer_rsrc_t r, uint32_t of
                      : "memory", "m0");
 }
 
-// ONCE: b is large and a row tile covers a segment, so b streams past the
-// caches (streams_b).
+// ONCE: b is large and (nearly) read once, so it streams past the caches
+// (streams_b).
 template <class T, int WM, int WN, int MI, int NI, int NBUF, bool ONCE>
 __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col_tiles)
 {
@@ -625,16 +625,28 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
 //   768 x 4096 x 4096 (32)     207    197   71.1    63.6    70.3   64.5   83.0
 //   3072 x 4096 x 4096 (32)    655    558    156     117     111   91.2    102
 //   12288 x 4096 x 4096 (32)  2457   2018    494     335     317    204    174
+// A call that reads b once, and more of it than the L2s hold twice over
+// (streams_b), takes its tiles from the last three, whose copies of b are
+// nontemporal; cached and not, us: 768 rows over 32 experts of 4096 x 4096 63.7
+// and 58.6, 512 rows 58.7 and 50.2, 64 rows 47.9 and 43.5, 3072 rows 91.2 and 85.0;
+// but dense, where row tiles share b, 512 rows 11.6 and 12.6, 2048 rows 26.1 and 28.2.
 struct Choice {
     int bm, bn, per_cu;
     double fix, step, fix1, step1;
 };
 constexpr Choice kChoices[] = {
-    {16, 16, 2, 2.0, 0.22, 2.0, 0.12},  {32, 16, 2, 2.0, 0.31, 2.0, 0.16},
-    {32, 64, 2, 1.5, 0.40, 1.5, 0.28},  {32, 128, 3, 3.0, 0.95, 2.0, 0.40},
-    {64, 128, 1, 2.5, 0.47, 2.5, 0.36}, {128, 128, 2, 5.0, 1.30, 4.0, 0.75},
-    {256, 256, 1, 6.0, 2.10, 6.0, 2.10},
+    {16, 16, 2, 2.0, 0.22, 2.0, 0.12},   {32, 16, 2, 2.0, 0.31, 2.0, 0.16},
+    {32, 64, 2, 1.5, 0.40, 1.5, 0.28},   {32, 128, 3, 3.0, 0.95, 2.0, 0.40},
+    {64, 128, 1, 2.5, 0.47, 2.5, 0.36},  {128, 128, 2, 5.0, 1.30, 4.0, 0.75},
+    {256, 256, 1, 6.0, 2.10, 6.0, 2.10}, {32, 128, 3, 3.0, 1.60, 2.0, 0.40},
+    {32, 128, 2, 3.0, 1.25, 2.0, 0.35},  {128, 128, 2, 5.0, 1.45, 4.0, 0.75},
 };
+constexpr int kNumChoices = sizeof(kChoices) / sizeof(kChoices[0]);
+
+bool streams_b(int E, int R, int N, int K)
+{
+    return (int64_t)E * N * (K / 2) > (INT64_C(64) << 20) && R <= (int64_t)E * 128;
+}
 
 // Row tiles of bm rows: exact for a dense product; over segments, whose
 // lengths only the device knows, the routed experts at least and half a tile
@@ -651,9 +663,12 @@ int choose(int E, int R, int N, int K, bool grouped)
 {
     constexpr int kUnits = 256;
     const double steps = (K + 255) / 256;
+    const bool once = streams_b(E, R, N, K);
     int best = 0;
     double least = 0.0;
-    for (int i = 0; i < (int)(sizeof(kChoices) / sizeof(kChoices[0])); ++i) {
+    for (int i = 0; i < kNumChoices; ++i) {
+        if (i >= 2 && (i >= 7) != once)
+            continue;
         const Choice& c = kChoices[i];
         const double tiles = row_tiles(E, R, grouped, c.bm) * ((N + c.bn - 1) / c.bn);
         const double us = tiles <= kUnits ? c.fix1 + c.step1 * steps
@@ -666,30 +681,21 @@ int choose(int E, int R, int N, int K, bool grouped)
     return best;
 }
 
-// Whether the tiles of bm rows read b (nearly) once, and more of it than the
-// L2s hold twice over: its copies are then nontemporal.  Measured cached and
-// not, us: 768 rows over 32 experts of 4096 x 4096 63.7 and 62.0, 600 rows 65.1
-// and 61.7, 64 rows 47.9 and 44.4, 768 rows over 64 experts of 2048 x 4096 68.0 and
-// 63.9; but dense, where row tiles share b, 512 rows 11.6 and 12.6, 2048 rows 26.1
-// and 28.2.
-bool streams_b(const MxGemmArgs& a, int bm)
-{
-    return (int64_t)a.E * a.N * (a.K / 2) > (INT64_C(64) << 20) && a.slots <= (int64_t)a.E * bm;
-}
-
 template <class T>
 hipError_t launch(const MxGemmArgs& a, hipStream_t s)
 {
     const int choice = choose(a.E, a.slots, a.N, a.K, a.offsets != nullptr);
-    const bool once = streams_b(a, kChoices[choice].bm);
     switch (choice) {
     case 0: return launch_few<T, 1, 1, 8, 2>(a, s);
     case 1: return launch_few<T, 2, 1, 8, 2>(a, s);
-    case 2: return once ? launch_tile<T, 1, 2, 1, 1, 4, true>(a, s) : launch_tile<T, 1, 2, 1, 1, 4>(a, s);
-    case 3: return once ? launch_tile<T, 1, 4, 1, 1, 2, true>(a, s) : launch_tile<T, 1, 4, 1, 1, 2>(a, s);
-    case 4: return once ? launch_tile<T, 2, 4, 1, 1, 3, true>(a, s) : launch_tile<T, 2, 4, 1, 1, 3>(a, s);
+    case 2: return launch_tile<T, 1, 2, 1, 1, 4>(a, s);
+    case 3: return launch_tile<T, 1, 4, 1, 1, 2>(a, s);
+    case 4: return launch_tile<T, 2, 4, 1, 1, 3>(a, s);
     case 5: return launch_tile<T, 2, 2, 2, 2, 2>(a, s);
-    default: return launch_tile<T, 2, 4, 4, 2, 2>(a, s);
+    case 6: return launch_tile<T, 2, 4, 4, 2, 2>(a, s);
+    case 7: return launch_tile<T, 1, 4, 1, 1, 2, true>(a, s);
+    case 8: return launch_tile<T, 1, 4, 1, 1, 3, true>(a, s);
+    default: return launch_tile<T, 2, 2, 2, 2, 2, true>(a, s);
     }
 }
 

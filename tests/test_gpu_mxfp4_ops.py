@@ -171,7 +171,7 @@ BY_TILE = [(11, 700, 1184, 0, (16, 16)), (29, 3000, 1056, 0, (32, 16)), (130, 15
            (12001, 1001, 992, 0, (256, 256)), (45, 2050, 480, 20, (32, 64)), (333, 4000, 1056, 40, (32, 128)),
            (2100, 600, 512, 20, (64, 128)), (6100, 1900, 544, 30, (128, 128)), (12300, 1000, 1024, 7, (256, 256)),
            # b read once and past the caches
-           (31, 7999, 4128, 5, (32, 64)), (31, 66010, 2080, 0, (32, 128)), (600, 4001, 2080, 17, (64, 128))]
+           (31, 7999, 4128, 5, (32, 128)), (31, 66010, 2080, 0, (32, 128)), (700, 3701, 2144, 17, (128, 128))]
 
 
 @pytest.mark.parametrize("rows,n,k,groups,tile", BY_TILE, ids=str)

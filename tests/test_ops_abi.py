@@ -134,7 +134,7 @@ def test_product_tiles():
     # measured points of the rule: the best or within 10 % of it
     for sizes, tile in (((1, 4096, 7168), 0), ((32, 4096, 4096), 1), ((128, 4096, 7168), 2),
                         ((512, 4096, 4096), 4), ((2048, 4096, 4096), 5), ((4096, 4096, 4096), 6),
-                        ((32, 4096, 4096, 32), 3), ((768, 4096, 4096, 32), 3),
+                        ((32, 4096, 4096, 32), 3), ((768, 4096, 4096, 32), 5), ((100, 2048, 2048, 16), 2),
                         ((6144, 4096, 4096, 32), 5), ((12288, 4096, 4096, 32), 6)):
         assert info(*sizes) == TILES[tile], sizes
     # every size has a tile
