@@ -128,7 +128,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t byte_rsrc(const uint8_t* p, ui
 // takes the 256-wide K steps w, w + WV, ... (so the workgroup reads WV * 128
 // consecutive bytes of each weight row at a time), straight from memory into
 // MFMA operands, D steps of each wave in flight, and the waves' sums meet in
-// LDS in wave order.  A step is two MFMAs per subtile pair: lane group g
+// LDS in wave order.  (One row by 4096 x 7168: 6.4 us on the device, 2.4 TB/s,
+// bound by the latency of a call that is over in a few loads; the host needs 7.)
+// A step is two MFMAs per subtile pair: lane group g
 // supplies K blocks 2 g and 2 g + 1 of the step's 8, so its two 16-byte loads
 // are adjacent and the four groups read one whole 128-byte line of each row.
 // Steps past the end are loads from outside the buffer resource: zeros.
@@ -281,6 +283,14 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
 // time; a byte permute of a row's 8 codes of one stage gives the MFMAs' scale
 // register for its four steps (lane group g takes codes 2 s + g, step s byte
 // s).  Codes past the end of K are 127, scale 1.
+//
+// 256 x 256 tiles at 8192 x 8192 x 7168: 233 to 239 us, 4.1 PFLOP/s.  Power bounds
+// them: the matrix cores alone sustain 6.2 PFLOP/s on random codes (9.2 on
+// zeros, where this call takes 190 us), and here they are busy half the cycles
+// at the clock that leaves.  Measured and not kept, us: four waves of 128 x 128
+// (297 against 280 on uniform codes), 64 x 128 per wave (285), copies spread over
+// three steps (290), raised wave priority (291), workgroups that walk tiles and
+// copy the next one's first stages early (288).
 constexpr int kCodeStages = 4;  // stages per load of scale codes
 
 template <class T, int WM, int WN, int MI, int NI, int NBUF>
@@ -611,25 +621,28 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
 // workgroups run `per_cu` to a compute unit, each fix + step * (256-wide K
 // steps) microseconds at that occupancy and fix1 + step1 * steps alone on its
 // unit, in whole rounds over the 256 units.  The figures are fits to a sweep
-// of 34 shapes (rows 1 to 12288, n and k 512 to 8192, 1 to 64 experts), where
-// the choice is within 10 % of the best of 16 tile shapes; some of its points,
-// us per call (7 us of them the host's share):
+// of 34 shapes (rows 1 to 12288, n and k 512 to 8192, 1 to 64 experts); over it
+// the choice is 2 % from the best of all (geometric mean), 12 % at worst, where
+// a call is host time.  Some of its points, us per call (7 of them the host's):
 //   rows x n x k (experts)   16x16  32x16  32x64  32x128  64x128  128^2  256^2
-//   1 x 4096 x 7168            7.7    7.4   11.1    17.1    13.2   21.3   37.3
-//   32 x 4096 x 4096           8.5    7.3    7.9     8.8     8.8   11.6   23.9
-//   128 x 4096 x 7168         43.8   33.8   12.1    18.7    15.3   24.5   39.7
-//   512 x 4096 x 4096          101   76.1   18.8    14.2    11.6   16.1   26.7
-//   2048 x 4096 x 4096         397    299   66.9    47.8    40.4   28.4   30.9
-//   4096 x 4096 x 4096         791    596    128    94.4    80.1   54.9   41.3
-//   32 x 4096 x 4096 (32)     52.2   71.5   36.8    31.5    39.5   46.3   65.2
-//   768 x 4096 x 4096 (32)     207    197   71.1    63.6    70.3   64.5   83.0
-//   3072 x 4096 x 4096 (32)    655    558    156     117     111   91.2    102
-//   12288 x 4096 x 4096 (32)  2457   2018    494     335     317    204    174
+//   1 x 4096 x 7168            7.8    7.7   11.0    16.5    13.0   20.6   37.2
+//   32 x 512 x 8192            9.1   10.6   11.2    14.2    13.8   18.9   40.9
+//   128 x 4096 x 7168         44.1   34.2   12.2    18.7    15.5   24.5   39.4
+//   300 x 8192 x 1024         43.7   38.0   11.2     7.5     8.6    7.9   11.5
+//   512 x 4096 x 4096          101   76.5   18.7    14.3    11.7   16.1   26.7
+//   2048 x 4096 x 4096         400    301   66.4    48.1    40.0   26.4   30.8
+//   4096 x 4096 x 4096         798    599    126    90.5    79.0   51.1   40.5
+//   6144 x 4096 x 4096 (32)   1261   1053    276     193     176    119    118
+//   12288 x 4096 x 4096 (32)  2469   2028    492     326     317    204    170
 // A call that reads b once, and more of it than the L2s hold twice over
-// (streams_b), takes its tiles from the last three, whose copies of b are
-// nontemporal; cached and not, us: 768 rows over 32 experts of 4096 x 4096 63.7
-// and 58.6, 512 rows 58.7 and 50.2, 64 rows 47.9 and 43.5, 3072 rows 91.2 and 85.0;
-// but dense, where row tiles share b, 512 rows 11.6 and 12.6, 2048 rows 26.1 and 28.2.
+// (streams_b), takes its tile from the last three kernels, whose copies of b
+// are nontemporal (32 x 128 with two and three buffers, 128^2); us:
+//   rows x n x k (experts)   cached 32x128   128^2   nt 32x128, 2   3   128^2
+//   32 x 4096 x 4096 (32)             31.3    46.0         29.3   35.5   45.1
+//   256 x 4096 x 4096 (32)            63.6    61.1         57.9   49.3   57.3
+//   768 x 4096 x 4096 (32)            63.4    64.1         61.4   64.2   59.6
+//   1536 x 4096 x 4096 (32)           85.8    76.6         94.1   95.0   70.5
+//   2048 x 4096 x 4096 (dense)        48.1    26.4         69.4   68.9   28.7
 struct Choice {
     int bm, bn, per_cu;
     double fix, step, fix1, step1;
