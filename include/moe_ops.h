@@ -123,14 +123,16 @@ int moe_dequantize_mxfp4(int32_t rows, int32_t cols, int32_t dtype, const uint8_
  *   a     uint8 [rows, k/2], a_sf uint8 [rows, k/32]
  *   b     uint8 [groups, n, k/2], b_sf uint8 [groups, n, k/32]
  *   y     [rows, n] bf16, f16 or f32 (dtype), row stride y_ld, rounded once
+ *         to nearest: a sum beyond the type's range becomes an infinity
  * Dense (offsets NULL, groups 1): every row.  Grouped: expert e's rows are
  * offsets[e] .. offsets[e] + counts[e] - 1 (counts NULL: up to
  * offsets[e + 1]), int32 device arrays as moe_route writes them; the rows of
  * y outside the segments (padding among them) are left as they were, and
  * a segment is cut at `rows`.  Segments do not overlap.  slots: an upper bound
  * of the rows of all segments together (T*K of the routing), for calls whose
- * `rows` counts a padded pool; it sizes the launch, so that rows beyond it may
- * be left as they were.  0: rows.  Dense calls ignore it.
+ * `rows` counts a padded pool; it sizes the launch and picks the tile (if the
+ * segments hold more, some of their rows are left as they were).  0: rows.
+ * Dense calls ignore it.
  * k % 32 == 0, 32 <= k <= 2^20, groups <= 1024, rows < 2^28, n < 2^28.
  * Scale code 0xFF on a block makes the sums it enters NaN.  a and b 16-byte
  * aligned.  y must not overlap an input.  Products and block sums are exact
@@ -145,7 +147,8 @@ int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
 
 /* Tile a moe_gemm_mxfp4 call of these sizes takes (host only): the rows and
  * columns of y per workgroup.  groups 0: dense; else that many segments, of
- * `rows` rows in all (a call's slots, if it states them).  Ranges as for moe_gemm_mxfp4; MOE_ERR_INVALID_ARG also for a null output. */
+ * `rows` rows in all (a call's slots, if it states them).  Ranges as for
+ * moe_gemm_mxfp4; MOE_ERR_INVALID_ARG also for a null output. */
 int moe_gemm_mxfp4_info(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t* tile_m,
                         int32_t* tile_n);
 

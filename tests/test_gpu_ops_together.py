@@ -189,6 +189,32 @@ def test_graph_replays():
             assert torch.equal(got, eager), k
 
 
+@pytest.mark.parametrize("rows,n,k,groups", [(3, 500, 512, 0), (300, 1000, 544, 4), (2047, 2100, 800, 0), (4200, 3000, 1056, 0)])
+def test_product_in_a_graph(rows, n, k, groups):
+    # (one size for each kind of kernel)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    q = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    a, a_sf = moe.moe_quantize_mxfp4(q(rows, k))
+    b, b_sf = moe.moe_quantize_mxfp4(q(max(1, groups) * n, k))
+    kw = {}
+    if groups:
+        b, b_sf = b.view(groups, n, -1), b_sf.view(groups, n, -1)
+        kw = dict(offsets=torch.linspace(0, rows, groups + 1, device="cuda").int())
+    run = lambda: moe.moe_gemm_mxfp4(a, a_sf, b, b_sf, **kw)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run()
+    for _ in range(3):
+        c, f = moe.moe_quantize_mxfp4(q(rows, k))
+        a.copy_(c), a_sf.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, run())
+
+
 def test_gradients_in_a_graph():
     T, K, E, W = 70, 4, 9, 200
     rng = np.random.default_rng(2)

@@ -191,6 +191,27 @@ def test_the_planner_lists_and_a_cut_list():
     assert dw.view(-1)[3] == 0 and dw.view(-1)[8] == 0
 
 
+def test_a_token_that_names_an_expert_twice():
+    T, K, E, W = 12, 4, 3, 50
+    rng = np.random.default_rng(9)
+    idx = rng.integers(0, E, (T, K))
+    idx[3] = 1
+    lists = ou.route(idx, E, 4)
+    d = ou.dev(lists)
+    x = torch.from_numpy(rng.standard_normal((T, W)).astype(np.float32))
+    before = torch.zeros(lists["pool"], W)
+    xp = moe.moe_permute(x.cuda(), d["row_src"], d["src_row"], d["offsets"], out=before.cuda())
+    same(xp, ou.permute(f64(x), lists, f64(before)))
+    w = torch.from_numpy(rng.random((T, K)).astype(np.float32))
+    check_sums(moe.moe_unpermute(xp, d["src_row"], T, w.cuda()), *ou.token_sums(f64(xp), lists, T, f64(w)), K,
+               torch.float32)
+    dyp, dw = moe.moe_unpermute_bwd(x.cuda(), xp, d["row_src"], d["src_row"], d["offsets"], w.cuda(),
+                                    dyp=before.cuda())
+    edyp, edw, mag = ou.unpermute_grads(f64(x), f64(xp), lists, f64(w), f64(before))
+    check_sums(dyp, edyp, abs(edyp), 1, torch.float32)
+    assert np.all(abs(f64(dw) - edw) <= (W / 64 + 14) * ou.U32 * mag)
+
+
 def test_no_tokens_and_all_masked():
     e = torch.empty(0, 32, device="cuda")
     none = torch.empty(0, dtype=torch.int32, device="cuda")
