@@ -99,12 +99,21 @@ def _rows(t, name, dev, dtype, rows, width):
     return ld if rows > 1 else width
 
 
+def _int32(name, *sizes):
+    """Refuses sizes the C ABI's int32 arguments cannot hold (ctypes would wrap them)."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{name}: {n}, beyond 32 bits")
+
+
 def _matrix(t, name, dtypes):
     """The dtype code and shape of an input matrix of rows."""
     if t.dim() != 2 or t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected [rows, width] of "
                          f"{', '.join(str(d) for d in dtypes)}")
-    return dtypes[t.dtype], t.shape[0], t.shape[1]
+    rows, width = t.shape
+    _int32(name, rows, width)
+    return dtypes[t.dtype], rows, width
 
 
 def _dense(t, name, dev, dtype, n):
@@ -120,6 +129,7 @@ def _dense(t, name, dev, dtype, n):
 def _slots(src_row, num_tokens, dev):
     """Checks src_row [T*K] (any shape); returns its address and K."""
     n = src_row.numel()
+    _int32("src_row", n)
     if num_tokens < 0 or (n % num_tokens or n == 0 if num_tokens else n):
         raise ValueError(f"src_row: {n} slots for {num_tokens} tokens")
     return _dense(src_row, "src_row", dev, torch.int32, n), n // num_tokens if num_tokens else 1
@@ -146,6 +156,7 @@ def moe_permute(x, row_src, src_row, offsets, out=None, stream=None):
     dt, T, W = _matrix(x, "x", _DTYPES_U8)
     src, K = _slots(src_row, T, dev)
     R = row_src.numel()
+    _int32("row_src", R)
     if out is None:
         out = torch.empty(R, W, dtype=x.dtype, device=x.device)
     _check(ops_lib().moe_permute(
@@ -203,6 +214,7 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
     dt, T, W = _matrix(dy, "dy", _DTYPES)
     src, K = _slots(src_row, T, dev)
     R = row_src.numel()
+    _int32("row_src", R)
     yp_at = dyp_at = dw_at = None
     yp_ld = dyp_ld = 0
     if need_dw:
@@ -248,6 +260,7 @@ def moe_dequantize_mxfp4(codes, sf, dtype=torch.bfloat16, out=None, stream=None)
     if codes.dim() != 2 or dtype not in _DTYPES:
         raise ValueError(f"codes: shape {tuple(codes.shape)}; dtype {dtype}")
     M, C = codes.shape[0], 2 * codes.shape[1]
+    _int32("codes", M, C)
     if out is None:
         out = torch.empty(M, C, dtype=dtype, device=codes.device)
     _check(ops_lib().moe_dequantize_mxfp4(
@@ -278,6 +291,7 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
     R, k2 = a.shape
     N, nb = b.shape[-2], k2 // 16
     E, lead = (1, ()) if offsets is None else (b.shape[0], (b.shape[0],))
+    _int32("sizes", E, R, N, 2 * k2, slots)
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     if dtype not in _DTYPES:
@@ -297,6 +311,7 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
 def moe_gemm_mxfp4_info(rows, n, k, groups=0):
     """Rows and columns of y per workgroup in a moe_gemm_mxfp4 call of these
     sizes (groups 0: dense), as {"tile_m", "tile_n"}."""
+    _int32("sizes", rows, n, k, groups)
     m, w = ctypes.c_int32(), ctypes.c_int32()
     _check(ops_lib().moe_gemm_mxfp4_info(groups, rows, n, k, ctypes.addressof(m),
                                          ctypes.addressof(w)), "moe_gemm_mxfp4_info")

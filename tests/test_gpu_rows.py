@@ -281,3 +281,22 @@ def test_binding_refusals():
         moe.moe_permute(yp[:8], d["row_src"], d["src_row"], d["offsets"], out=yp)
     with pytest.raises(moe.MoEError):
         moe.moe_unpermute_bwd(x, None, d["row_src"], d["src_row"], d["offsets"], need_dyp=False, need_dw=False)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    # (their low 32 bits alone would name a small call that fits)
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    wide = torch.empty(1, (1 << 32) + 32, dtype=torch.uint8, device="cuda")
+    half = wide.view(torch.float16)
+    u = torch.zeros(1, 16, dtype=torch.uint8, device="cuda")
+    sf = torch.zeros(1, 1, dtype=torch.uint8, device="cuda")
+    for f in (lambda: moe.moe_permute(wide, i, i, None), lambda: moe.moe_permute_bwd(half, i, 1),
+              lambda: moe.moe_quantize_mxfp4(half), lambda: moe.moe_dequantize_mxfp4(wide, sf),
+              lambda: moe.moe_gemm_mxfp4(wide[:, :-16], sf, u, sf),
+              lambda: moe.moe_gemm_mxfp4(u, sf, wide.view(-1, 16), sf),
+              lambda: moe.moe_gemm_mxfp4(u, sf, u[None], sf[None], offsets=torch.cat([i, i]), slots=(1 << 32) + 1)):
+        with pytest.raises((ValueError, moe.MoEError)) as e:
+            f()
+        print(e.value)
+    del wide, half
+    torch.cuda.empty_cache()

@@ -147,5 +147,10 @@ def test_product_tiles():
         with pytest.raises(moe.MoEError) as e:
             info(*bad)
         assert e.value.code == code
+    for at in range(4):                                    # not wrapped into range
+        sizes = [4, 4, 32, 1]
+        sizes[at] += 1 << 32
+        with pytest.raises(ValueError, match="beyond 32 bits"):
+            info(*sizes)
     m = ctypes.c_int32()
     assert ops.ops_lib().moe_gemm_mxfp4_info(0, 4, 4, 32, None, ctypes.addressof(m)) == INV
