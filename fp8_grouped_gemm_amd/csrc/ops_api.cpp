@@ -295,7 +295,8 @@ int moe_gemm_mxfp4(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
         return rc;
     moe::MxGemmArgs g{};
     g.E = groups; g.R = rows; g.N = n; g.K = k; g.dtype = dtype;
-    g.slots = offsets && slots > 0 && slots < rows ? slots : rows;
+    // (without counts the segments take in their padding, which slots leaves out)
+    g.slots = offsets && counts && slots > 0 && slots < rows ? slots : rows;
     g.a = a; g.a_sf = a_sf; g.b = b; g.b_sf = b_sf;
     g.offsets = offsets; g.counts = counts;
     g.y = static_cast<char*>(y);

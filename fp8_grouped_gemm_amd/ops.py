@@ -277,8 +277,8 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
     with offsets int32 [E+1] and counts int32 [E] (None: the segments'
     whole lengths): expert e's rows offsets[e] .. + counts[e], the other rows
     of y left as they were (a new y: unset).  y's type: out's, else dtype,
-    else bf16.  slots: an upper bound of the rows of all segments together
-    (T * K), where a pool with padding has more rows than that (0: R)."""
+    else bf16.  slots: an upper bound of the counts' sum (T * K), where a pool
+    with padding has more rows than that (0: R; without counts not used)."""
     if not _here(a, stream):
         return _elsewhere(moe_gemm_mxfp4, a, stream, a, a_sf, b, b_sf, offsets, counts, dtype, out,
                           slots)

@@ -15,8 +15,11 @@
  * current device, every argument checked on the host before any HIP call,
  * MOE_OK or a negative MOE_ERR_* code returned.  What differs: no plan (the
  * shapes are arguments), no workspace, and the matrices of bf16 / f16 / f32
- * rows have a row stride (`*_ld`, in elements, at least the row's width and at most 2^30;
- * 0 = densely packed).  Rows need only the alignment of their element type.
+ * rows have a row stride (`*_ld`, in elements, at least the row's width and at
+ * most 2^30; 0 = densely packed).  Rows need only the alignment of their
+ * element type.  Where an output must not overlap another tensor, that counts
+ * whole spans, from a matrix's first element to its last, the gaps between
+ * its rows among them.
  * No entry point uses atomics on results: equal calls give equal bits.
  * Every call may be captured into a HIP graph and replayed, and calls on
  * different streams are independent as long as their outputs are.
@@ -129,10 +132,10 @@ int moe_dequantize_mxfp4(int32_t rows, int32_t cols, int32_t dtype, const uint8_
  * offsets[e + 1]), int32 device arrays as moe_route writes them; the rows of
  * y outside the segments (padding among them) are left as they were, and
  * a segment is cut at `rows`.  Segments do not overlap.  slots: an upper bound
- * of the rows of all segments together (T*K of the routing), for calls whose
- * `rows` counts a padded pool; it sizes the launch and picks the tile (if the
- * segments hold more, some of their rows are left as they were).  0: rows.
- * Dense calls ignore it.
+ * of the counts' sum (T*K of the routing), for calls whose `rows` counts a
+ * padded pool; it sizes the launch and picks the tile (if the counts hold more,
+ * some of their rows are left as they were).  0: rows.  Calls without counts,
+ * whose segments take in their padding, and dense ones ignore it.
  * k % 32 == 0, 32 <= k <= 2^20, groups <= 1024, rows < 2^28, n < 2^28.
  * Scale code 0xFF on a block makes the sums it enters NaN.  a and b 16-byte
  * aligned.  y must not overlap an input.  Products and block sums are exact

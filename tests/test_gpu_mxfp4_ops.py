@@ -278,6 +278,13 @@ def test_grouped_product(lens, n, k, align):
     if align == 1:                                          # whole segments without counts
         z = torch.full_like(y, 55.0)
         assert torch.equal(moe.moe_gemm_mxfp4(*d, out=z), y)
+    # without counts the padding rows belong to the segments, whatever slots says
+    a2, asf2 = d[0], torch.where(d[1] == 255, 127, d[1])
+    unset = torch.full_like(y, float("nan"))
+    whole = [moe.moe_gemm_mxfp4(a2, asf2, *d[2:], out=unset.clone(), slots=v) for v in (0, 1, sum(lens))]
+    used = int(offsets[-1])
+    for z in whole:
+        assert torch.equal(z[:used], whole[0][:used]) and torch.all(torch.isnan(z[used:]))
 
 
 @pytest.mark.parametrize("rows", [6, 40, 200, 900])
