@@ -76,7 +76,9 @@ __device__ __forceinline__ RowTile pick_tile(const MxGemmArgs& a, int col_tiles,
                 segment(a, e0 + lane, first, n);
             tiles = (n + BM - 1) / BM;
             upto = lane_sums(tiles, lane);
-            row_tiles += __builtin_amdgcn_readlane(upto, 63);
+            // (at most 2^30 in 64 segments; the cap, which segments that do not
+            // overlap keep below, holds every sum of them inside 32 bits)
+            row_tiles = min(row_tiles + __builtin_amdgcn_readlane(upto, 63), a.R / BM + a.E);
         }
     }
     const int total = row_tiles * col_tiles;

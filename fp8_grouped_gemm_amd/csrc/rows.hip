@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int 
 #pragma unroll
     for (int i = 0; i < E::VEC; ++i)
         acc[i] = 0.f;
-        constexpr int U = 4;
+    constexpr int U = 4;
     for (int j0 = 0; j0 < a.K; j0 += U) {
         float v[U][E::VEC], wt[U];
         bool on[U];

@@ -314,6 +314,38 @@ def test_nan_scales_and_cut_segments(rows):
     assert np.all(abs(got - ex)[fine] <= bound(k, mag, ex, torch.float32)[fine])
 
 
+@pytest.mark.parametrize("rows,n", [(1, (1 << 28) - 1), (3, (1 << 27) + 5), ((1 << 28) - 1, 1), ((1 << 27) + 300, 3)])
+def test_largest_sizes(rows, n):
+    # One block of K: sums of 32 products of e2m1 values under one scale are exact in
+    # f32, whatever the tile, so pieces of the long side can be compared as calls of their own.
+    say(f"product {rows} x {n} x 32")
+    side = max(rows, n)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    wide = torch.randint(0, 256, (side, 16), dtype=torch.uint8, device="cuda", generator=g)
+    wide_sf = torch.randint(120, 134, (side, 1), dtype=torch.uint8, device="cuda", generator=g)
+    few, few_sf = wide[1000:1000 + min(rows, n)].clone(), wide_sf[1000:1000 + min(rows, n)].clone()
+    call = lambda w, f: (moe.moe_gemm_mxfp4(few, few_sf, w, f) if n > rows else moe.moe_gemm_mxfp4(w, f, few, few_sf))
+    y = call(wide, wide_sf)
+    for at in (0, 65536, (1 << 26) - 500, (1 << 27) - 777, side - 1001):
+        part = call(wide[at:at + 1001], wide_sf[at:at + 1001].clone())
+        assert torch.equal(y[:, at:at + 1001] if n > rows else y[at:at + 1001], part), at
+    del wide, wide_sf, y
+    torch.cuda.empty_cache()
+
+
+def test_segments_that_overlap():
+    # (not allowed; whatever they leave in their rows, the others stay)
+    rows, n, k, E = 300, 40, 64, 130
+    d = [torch.randint(0, 128, s, dtype=torch.uint8, device="cuda")
+         for s in ((rows, k // 2), (rows, k // 32), (E, n, k // 2), (E, n, k // 32))]
+    off = torch.full((E + 1,), 20, dtype=torch.int32, device="cuda")
+    cnt = torch.full((E,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    for slots in (0, 7):
+        y = torch.full((rows + 1, n), 5.0, device="cuda")
+        moe.moe_gemm_mxfp4(*d, offsets=off, counts=cnt, slots=slots, out=y[:rows])
+        assert torch.all(y[:20] == 5) and torch.all(y[rows] == 5)
+
+
 def test_product_refusals():
     u = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")
     i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
