@@ -115,6 +115,21 @@ def test_quantise_strided_rows(dtype):
     assert torch.all(out[:, 0] == 9) and torch.all(out[:, 161:] == 9)
 
 
+@pytest.mark.parametrize("rows,cols", [((1 << 26) + 77, 32), (3, (1 << 24) - 32), (70000, 33024)])
+def test_quantise_past_32_bit_offsets(rows, cols):
+    say(f"quantise {rows} x {cols}")
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    codes, sf = moe.moe_quantize_mxfp4(x)
+    back = moe.moe_dequantize_mxfp4(codes, sf)
+    for at in (0, rows // 2, max(0, rows - 100)):
+        s = slice(at, at + 100)
+        c, f = moe.moe_quantize_mxfp4(x[s].clone())
+        assert torch.equal(codes[s], c) and torch.equal(sf[s], f)
+        assert torch.equal(back[s], moe.moe_dequantize_mxfp4(c, f))
+    del x, codes, sf, back
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- product
 
 # One MFMA rounds its running f32 sum with an error of at most 2^-22 of the
