@@ -292,7 +292,9 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
 // at the clock that leaves.  Measured and not kept, us: four waves of 128 x 128
 // (297 against 280 on uniform codes), 64 x 128 per wave (285), copies spread over
 // three steps (290), raised wave priority (291), workgroups that walk tiles and
-// copy the next one's first stages early (288).
+// copy the next one's first stages early (288).  Tiles between the ones kept: 192 x 256
+// 317 here and 203 for 196 at 12288 rows over 32 experts of 4096 x 4096 (112 for 118 at
+// 6144), 128 x 256 395 and 241 (24.3 for 26.0 at 2048 x 4096 x 4096).
 constexpr int kCodeStages = 4;  // stages per load of scale codes
 
 template <class T, int WM, int WN, int MI, int NI, int NBUF>

@@ -99,11 +99,14 @@ def _rows(t, name, dev, dtype, rows, width):
     return ld if rows > 1 else width
 
 
-def _int32(name, *sizes):
-    """Refuses sizes the C ABI's int32 arguments cannot hold (ctypes would wrap them)."""
-    for n in sizes:
-        if not -(1 << 31) <= n < 1 << 31:
-            raise ValueError(f"{name}: {n}, beyond 32 bits")
+_MAX = (1 << 31) - 1
+
+
+def _int32(name, size):
+    """Refuses a size (the largest of a call's) that the C ABI's int32 arguments
+    cannot hold: ctypes would wrap it."""
+    if size > _MAX:
+        raise ValueError(f"{name}: {size}, beyond 32 bits")
 
 
 def _matrix(t, name, dtypes):
@@ -112,7 +115,7 @@ def _matrix(t, name, dtypes):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected [rows, width] of "
                          f"{', '.join(str(d) for d in dtypes)}")
     rows, width = t.shape
-    _int32(name, rows, width)
+    _int32(name, max(rows, width))
     return dtypes[t.dtype], rows, width
 
 
@@ -260,7 +263,7 @@ def moe_dequantize_mxfp4(codes, sf, dtype=torch.bfloat16, out=None, stream=None)
     if codes.dim() != 2 or dtype not in _DTYPES:
         raise ValueError(f"codes: shape {tuple(codes.shape)}; dtype {dtype}")
     M, C = codes.shape[0], 2 * codes.shape[1]
-    _int32("codes", M, C)
+    _int32("codes", max(M, C))
     if out is None:
         out = torch.empty(M, C, dtype=dtype, device=codes.device)
     _check(ops_lib().moe_dequantize_mxfp4(
@@ -291,7 +294,7 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
     R, k2 = a.shape
     N, nb = b.shape[-2], k2 // 16
     E, lead = (1, ()) if offsets is None else (b.shape[0], (b.shape[0],))
-    _int32("sizes", E, R, N, 2 * k2, slots)
+    _int32("sizes", max(E, R, N, 2 * k2, abs(slots)))
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     if dtype not in _DTYPES:
@@ -311,7 +314,7 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
 def moe_gemm_mxfp4_info(rows, n, k, groups=0):
     """Rows and columns of y per workgroup in a moe_gemm_mxfp4 call of these
     sizes (groups 0: dense), as {"tile_m", "tile_n"}."""
-    _int32("sizes", rows, n, k, groups)
+    _int32("sizes", max(map(abs, (rows, n, k, groups))))
     m, w = ctypes.c_int32(), ctypes.c_int32()
     _check(ops_lib().moe_gemm_mxfp4_info(groups, rows, n, k, ctypes.addressof(m),
                                          ctypes.addressof(w)), "moe_gemm_mxfp4_info")
