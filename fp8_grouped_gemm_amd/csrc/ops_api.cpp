@@ -202,7 +202,8 @@ int moe_unpermute_bwd(int32_t T, int32_t K, int32_t R, int32_t width, int32_t dt
     const int es = elem_bytes(dtype);
     const int64_t dld = stride(dy_ld, width), yld = dw ? stride(yp_ld, width) : 0,
                   old = dyp ? stride(dyp_ld, width) : 0;
-    if ((!dyp && !dw) || dld < 0 || yld < 0 || old < 0 || (T > 0 && (!dy || !src_row)) ||
+    // (without tokens or pool rows a requested output may be empty, its address null)
+    if ((!dyp && !dw && T > 0 && R > 0) || dld < 0 || yld < 0 || old < 0 || (T > 0 && (!dy || !src_row)) ||
         (T > 0 && dw && !yp && R > 0) || misaligned(dy, es) || (dw && misaligned(yp, es)) ||
         misaligned(dyp, es) || misaligned(dw, 4) || misaligned(topk_w, 4) ||
         misaligned(row_src, 4) || misaligned(src_row, 4) || misaligned(used, 4))
@@ -217,7 +218,7 @@ int moe_unpermute_bwd(int32_t T, int32_t K, int32_t R, int32_t width, int32_t dt
             return MOE_ERR_INVALID_ARG;
     if (overlap(op, ow))
         return MOE_ERR_INVALID_ARG;
-    if (T == 0 && (!dyp || !row_src || R == 0))
+    if ((!dyp && !dw) || (T == 0 && (!dyp || !row_src || R == 0)))
         return MOE_OK;
     rc = moe::device_status();
     if (rc != MOE_OK)

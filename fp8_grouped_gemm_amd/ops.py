@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import _check, lib
+from . import MOE_ERR_INVALID_ARG, _check, lib
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
@@ -214,6 +214,8 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
         return _elsewhere(moe_unpermute_bwd, dy, stream, dy, yp, row_src, src_row, offsets, topk_w,
                           dyp, dw, need_dyp, need_dw)
     dev = dy.get_device()
+    if not (need_dyp or need_dw):
+        _check(MOE_ERR_INVALID_ARG, "moe_unpermute_bwd")
     dt, T, W = _matrix(dy, "dy", _DTYPES)
     src, K = _slots(src_row, T, dev)
     R = row_src.numel()
@@ -223,7 +225,9 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
     if need_dw:
         yp_at, yp_ld = yp.data_ptr(), _rows(yp, "yp", dev, dy.dtype, R, W)
         if dw is None:
-            dw = torch.empty(T, K, dtype=torch.float32, device=dy.device)
+            # (no tokens: src_row is empty and only topk_w knows the slots per token)
+            k = topk_w.shape[1] if T == 0 and topk_w is not None and topk_w.dim() == 2 else K
+            dw = torch.empty(T, k, dtype=torch.float32, device=dy.device)
         dw_at = _dense(dw, "dw", dev, torch.float32, T * K)
     if need_dyp:
         if dyp is None:

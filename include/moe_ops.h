@@ -90,7 +90,8 @@ int moe_unpermute(int32_t num_tokens, int32_t top_k, int32_t pool_rows, int32_t 
  *                           *used on left as they were; NULL: not computed
  *   dw  f32 [T, K]          dot of dy[f / K] and yp[src_row[f]] in f32, 0 for a masked
  *                           slot; NULL: not computed (yp and its stride are then unused)
- * At least one of dyp and dw.  row_src and used serve dyp only (NULL
+ * At least one of dyp and dw, unless T or pool_rows is 0 (an empty output may have
+ * no address; the call then does what is left, if anything).  row_src and used serve dyp only (NULL
  * row_src: padding rows are left as they were).  topk_w NULL: every weight 1.
  * Neither output may overlap an input or the other.
  */
