@@ -83,7 +83,8 @@ __device__ __forceinline__ RowTile pick_tile(const MxGemmArgs& a, int col_tiles,
     }
     const int total = row_tiles * col_tiles;
     const int share = (total + 7) / 8;
-    const int i = blockIdx.x / 8, at = (blockIdx.x % 8) * share + i;
+    const int wg = workgroup();
+    const int i = wg / 8, at = (wg % 8) * share + i;
     if (i >= share || at >= total)
         return {0, 0, 0};
     const int band = at / (kBand * col_tiles), in = at - band * kBand * col_tiles;
@@ -600,7 +601,7 @@ hipError_t launch_few(const MxGemmArgs& a, hipStream_t s)
     const unsigned grid = tile_grid(a, 16 * MT, ct);
     if (!grid)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((mxfp4_rows<T, MT, NT, WV, D>), dim3(grid), dim3(64 * WV), 0, s, a, ct);
+    hipLaunchKernelGGL((mxfp4_rows<T, MT, NT, WV, D>), grid_of(grid), dim3(64 * WV), 0, s, a, ct);
     return hipGetLastError();
 }
 
@@ -617,7 +618,7 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
                                              hipFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(C::TH), C::SMEM, s, a, ct);
+    hipLaunchKernelGGL(kernel, grid_of(grid), dim3(C::TH), C::SMEM, s, a, ct);
     return hipGetLastError();
 }
 

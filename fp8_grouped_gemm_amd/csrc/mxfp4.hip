@@ -59,9 +59,9 @@ bool streams(const MxQuantArgs& a, int size)
 template <int VEC>
 __device__ __forceinline__ bool place(const MxQuantArgs& a, int tpr, int pieces, int64_t& row, int& col)
 {
-    const unsigned g = blockIdx.x / pieces;
+    const unsigned wg = workgroup(), g = wg / pieces;
     row = (int64_t)g * (kThreads / tpr) + threadIdx.x / tpr;
-    col = ((blockIdx.x - g * pieces) * tpr + threadIdx.x % tpr) * VEC;
+    col = ((wg - g * pieces) * tpr + threadIdx.x % tpr) * VEC;
     return row < a.rows && col < a.cols;
 }
 
@@ -144,7 +144,7 @@ hipError_t launch(const MxQuantArgs& a, bool back, hipStream_t s)
     const bool nt = streams(a, E::SIZE);
     const auto kernel = back ? (nt ? dequantize_mxfp4<E, true> : dequantize_mxfp4<E, false>)
                              : (nt ? quantize_mxfp4<E, true> : quantize_mxfp4<E, false>);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
+    hipLaunchKernelGGL(kernel, grid_of(wgs), dim3(kThreads), 0, s, a, tpr, pieces);
     return hipGetLastError();
 }
 

@@ -55,6 +55,19 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs& a, hipStream_t s);
 // Tile of a call (host only): only E, R, N, K and whether it is grouped count.
 void gemm_mxfp4_tile(int E, int R, int N, int K, bool grouped, int& bm, int& bn);
 
+// A launch takes fewer than 2^32 threads along an axis: of its workgroups (up to
+// 1024 threads each), numbered through, those from 2^kGridBits on go along y.
+// The grid is whole rows of them, so a kernel ignores numbers past its last.
+constexpr int kGridBits = 21;
+
+inline dim3 grid_of(int64_t wgs)
+{
+    const int64_t row = INT64_C(1) << kGridBits;
+    return wgs <= row ? dim3((unsigned)wgs) : dim3((unsigned)row, (unsigned)((wgs + row - 1) / row));
+}
+
+__device__ __forceinline__ unsigned workgroup() { return (blockIdx.y << kGridBits) + blockIdx.x; }
+
 // MOE_OK if the current device is gfx950 (moe_api.cpp).
 int device_status();
 

@@ -90,14 +90,15 @@ template <bool NT>
 __global__ __launch_bounds__(kThreads) void permute_rows(RowsArgs a, int row_bytes, int tpr,
                                                          int pieces, unsigned token_wgs)
 {
-    if (blockIdx.x >= token_wgs) {
-        const int wave = (blockIdx.x - token_wgs) * (kThreads / 64) + (threadIdx.x >> 6);
+    const unsigned wg = workgroup();
+    if (wg >= token_wgs) {
+        const int wave = (wg - token_wgs) * (kThreads / 64) + (threadIdx.x >> 6);
         clear_padding<NT>(a, wave * kPadRows, row_bytes, threadIdx.x & 63);
         return;
     }
-    const unsigned g = blockIdx.x / pieces;
+    const unsigned g = wg / pieces;
     const int t = g * (kThreads / tpr) + threadIdx.x / tpr;
-    int at = ((blockIdx.x - g * pieces) * tpr + threadIdx.x % tpr) * 16;
+    int at = ((wg - g * pieces) * tpr + threadIdx.x % tpr) * 16;
     if (t >= a.T || at >= row_bytes)
         return;
     const char* src = a.tok + (int64_t)t * a.tok_ld;
@@ -126,9 +127,9 @@ __global__ __launch_bounds__(kThreads) void permute_rows(RowsArgs a, int row_byt
 template <class E, bool W, bool NT>
 __global__ __launch_bounds__(kThreads) void token_sums(RowsArgs a, int tpr, int pieces)
 {
-    const unsigned g = blockIdx.x / pieces;
+    const unsigned wg = workgroup(), g = wg / pieces;
     const int t = g * (kThreads / tpr) + threadIdx.x / tpr;
-    const int c = ((blockIdx.x - g * pieces) * tpr + threadIdx.x % tpr) * E::VEC;
+    const int c = ((wg - g * pieces) * tpr + threadIdx.x % tpr) * E::VEC;
     if (t >= a.T || c >= a.width)
         return;
     const int n = a.width - c;
@@ -172,12 +173,13 @@ __global__ __launch_bounds__(kThreads) void unpermute_grad(RowsArgs a, unsigned 
 {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (blockIdx.x >= token_wgs) {
-        clear_padding<NT>(a, ((blockIdx.x - token_wgs) * (kThreads / 64) + wave) * kPadRows,
+    const unsigned wg = workgroup();
+    if (wg >= token_wgs) {
+        clear_padding<NT>(a, ((wg - token_wgs) * (kThreads / 64) + wave) * kPadRows,
                       a.width * E::SIZE, lane);
         return;
     }
-    const int f = blockIdx.x * (kThreads / 64) + wave;
+    const int f = wg * (kThreads / 64) + wave;
     if (f >= a.T * a.K)
         return;
     const int r = a.src_row[f];
@@ -234,7 +236,7 @@ hipError_t launch_permute(const RowsArgs& a, hipStream_t s)
     if (wgs + pad == 0)
         return hipSuccess;
     const auto kernel = streams(a, a.pool_out, a.pool_out_ld, size) ? permute_rows<true> : permute_rows<false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs + pad), dim3(kThreads), 0, s, a, row_bytes, tpr, pieces,
+    hipLaunchKernelGGL(kernel, grid_of(wgs + pad), dim3(kThreads), 0, s, a, row_bytes, tpr, pieces,
                        (unsigned)wgs);
     return hipGetLastError();
 }
@@ -251,7 +253,7 @@ static hipError_t launch_token_sums(const RowsArgs& a, hipStream_t s)
     const bool nt = streams(a, a.pool, a.pool_ld, E::SIZE);
     const auto kernel = a.w ? (nt ? token_sums<E, true, true> : token_sums<E, true, false>)
                             : (nt ? token_sums<E, false, true> : token_sums<E, false, false>);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a, tpr, pieces);
+    hipLaunchKernelGGL(kernel, grid_of(wgs), dim3(kThreads), 0, s, a, tpr, pieces);
     return hipGetLastError();
 }
 
@@ -270,7 +272,7 @@ static hipError_t launch_grad(const RowsArgs& a, hipStream_t s)
 {
     const unsigned wgs = (unsigned)(((int64_t)a.T * a.K + kThreads / 64 - 1) / (kThreads / 64));
     const unsigned pad = a.pool_out ? pad_wgs(a) : 0u;
-    const dim3 grid(wgs + pad), block(kThreads);
+    const dim3 grid = grid_of((int64_t)wgs + pad), block(kThreads);
     if (wgs + pad == 0)
         return hipSuccess;
     bool nt = true;

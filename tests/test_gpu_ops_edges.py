@@ -51,3 +51,102 @@ def test_every_slot_masked_and_an_empty_pool(dtype):
     assert dyp.shape == (0, W) and dw is None
     dyp, dw = moe.moe_unpermute_bwd(dy, pool, none, src_row, offsets, need_dyp=False)
     assert dyp is None and torch.all(dw == 0)
+
+
+# Launches of 2^32 threads and more, whose workgroups go on along the grid's y axis.
+
+def done(*tensors):
+    for t in tensors:
+        t.untyped_storage().resize_(0)
+    torch.cuda.empty_cache()
+
+
+def test_padding_of_the_largest_pool():
+    R = (1 << 28) - 1                                         # 2^24 workgroups look for padding
+    say(f"padding of {R} pool rows")
+    rows = [R - 1, 0, 1 << 27, -1, 5, R - 2]                  # of 3 tokens, top-2
+    src_row, row_src = ints(*rows), torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    for f, r in enumerate(rows):
+        if r >= 0:
+            row_src[r] = f
+    x = torch.tensor([[11], [22], [33]], dtype=torch.uint8, device="cuda")
+    xp = torch.full((R, 1), 7, dtype=torch.uint8, device="cuda")
+    moe.moe_permute(x, row_src, src_row, None, out=xp)
+    want = torch.zeros_like(xp)
+    for f, r in enumerate(rows):
+        if r >= 0:
+            want[r] = x[f // 2]
+    assert torch.equal(xp, want)
+    done(xp, want)
+    dy, yp = torch.tensor([[2.0], [4.0], [8.0]], device="cuda").bfloat16(), torch.ones(R, 1, device="cuda").bfloat16()
+    dyp = torch.full_like(yp, 7.0)
+    _, dw = moe.moe_unpermute_bwd(dy, yp, row_src, src_row, None, dyp=dyp)
+    for f, r in enumerate(rows):
+        assert dw.view(-1)[f] == (dy[f // 2] if r >= 0 else 0)
+        if r >= 0:
+            assert dyp[r] == dy[f // 2]
+            dyp[r] = 0
+    assert not dyp.any()
+    done(yp, dyp, row_src)
+
+
+def test_sums_of_the_most_tokens():
+    T, W = 1 << 23, 1028                                      # two workgroups a token: 2^24
+    say(f"sums of {T} tokens of {W} f32")
+    pool = torch.randn(3, W, device="cuda")
+    src_row = (torch.arange(T, device="cuda") * 7 % 4 - 1).int()        # every fourth is masked
+    y = moe.moe_unpermute(pool, src_row, T)
+    rows = torch.cat([torch.zeros(1, W, device="cuda"), pool])
+    for at in range(0, T, T // 8):
+        s = slice(at, at + T // 8)
+        assert torch.equal(y[s], rows[src_row[s].long() + 1]), at
+    done(y)
+
+
+def test_permute_of_the_most_tokens():
+    T, W, R = 1 << 23, 4100, 5
+    say(f"permute {T} tokens of {W} bytes")
+    x = torch.zeros(T, W, dtype=torch.uint8, device="cuda")
+    src_row = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    row_src = ints(0, 1 << 22, -1, T - 1, T - 2)
+    for r, f in enumerate(row_src.tolist()):
+        if f >= 0:
+            src_row[f] = r
+            x[f] = torch.randint(0, 256, (W,), device="cuda").to(torch.uint8)
+    xp = moe.moe_permute(x, row_src, src_row, None, out=torch.full((R, W), 7, dtype=torch.uint8, device="cuda"))
+    for r, f in enumerate(row_src.tolist()):
+        assert torch.equal(xp[r], x[f] if f >= 0 else torch.zeros_like(xp[r])), r
+    done(x)
+
+
+def test_quantise_the_most_rows():
+    rows, cols = (1 << 29) + 77, 32                           # 32 rows a workgroup
+    say(f"quantise {rows} x {cols}")
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    codes, sf = moe.moe_quantize_mxfp4(x)
+    back = torch.full_like(x, float("nan"))
+    moe.moe_dequantize_mxfp4(codes, sf, out=back)
+    for at in (0, 1 << 28, (1 << 29) - 50, rows - 100):
+        s = slice(at, at + 100)
+        c, f = moe.moe_quantize_mxfp4(x[s].clone())
+        assert torch.equal(codes[s], c) and torch.equal(sf[s], f), at
+        assert torch.equal(back[s], moe.moe_dequantize_mxfp4(c, f)), at
+    done(x, codes, sf, back)
+
+
+def test_product_of_the_most_tiles():
+    # one row for each of 1024 experts: 2^24 tiles and more of 32 x 128.  (One block of K: sums
+    # exact in f32 whatever the tile, so each expert's row equals its own dense product's.)
+    E, N, K = 1024, (1 << 21) + 129, 32
+    say(f"{E} segments of one row, {N} columns")
+    assert tuple(moe.moe_gemm_mxfp4_info(E, N, K, E).values()) == (32, 128)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    u = lambda lo, hi, *s: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda", generator=g)
+    a, a_sf = u(0, 256, E, K // 2), u(120, 134, E, 1)
+    b, b_sf = u(0, 256, E, N, K // 2), u(120, 134, E, N, 1)
+    y = moe.moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=torch.arange(E + 1, dtype=torch.int32, device="cuda"),
+                           out=torch.full((E, N), float("nan"), dtype=torch.bfloat16, device="cuda"))
+    for e in (0, 1, 500, E - 2, E - 1):
+        assert torch.equal(y[e:e + 1], moe.moe_gemm_mxfp4(a[e:e + 1], a_sf[e:e + 1], b[e], b_sf[e])), e
+    assert not torch.isnan(y).any()
+    done(b, b_sf, y)
