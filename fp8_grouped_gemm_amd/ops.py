@@ -209,7 +209,9 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
     """Gradients of moe_unpermute for dy [T, W]: (dyp [pool_rows, W], dw f32
     [T, K]); dyp's padding rows below offsets[-1] are zeros, its rows from
     there on left as they were.  need_dyp / need_dw False: that one is None
-    (without need_dw, yp is not read and may be None)."""
+    (without need_dw, yp is not read and may be None).  row_src None: dyp's
+    padding rows are left as they were too (a new dyp: unset), and the pool has
+    as many rows as yp, or as dyp where there is no yp."""
     if not _here(dy, stream):
         return _elsewhere(moe_unpermute_bwd, dy, stream, dy, yp, row_src, src_row, offsets, topk_w,
                           dyp, dw, need_dyp, need_dw)
@@ -218,7 +220,12 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
         _check(MOE_ERR_INVALID_ARG, "moe_unpermute_bwd")
     dt, T, W = _matrix(dy, "dy", _DTYPES)
     src, K = _slots(src_row, T, dev)
-    R = row_src.numel()
+    if need_dw and yp is None:
+        raise ValueError("yp: None, needed for dw (need_dw=False leaves dw out)")
+    pool = next((t for t in (row_src, yp, dyp) if t is not None), None)
+    if pool is None:
+        raise ValueError("none of row_src, yp and dyp, which the pool's rows are known by")
+    R = row_src.numel() if row_src is not None else pool.shape[0] if pool.dim() else 0
     _int32("row_src", R)
     yp_at = dyp_at = dw_at = None
     yp_ld = dyp_ld = 0
@@ -235,7 +242,8 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
         dyp_at, dyp_ld = dyp.data_ptr(), _rows(dyp, "dyp", dev, dy.dtype, R, W)
     _check(ops_lib().moe_unpermute_bwd(
         T, K, R, W, dt, dy.data_ptr(), _rows(dy, "dy", dev, dy.dtype, T, W), yp_at, yp_ld,
-        _dense(row_src, "row_src", dev, torch.int32, R), src, _used(offsets, dev),
+        None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), src,
+        _used(offsets, dev),
         None if topk_w is None else _dense(topk_w, "topk_w", dev, torch.float32, T * K),
         dyp_at, dyp_ld, dw_at, _raw_stream(dev)), "moe_unpermute_bwd")
     return (dyp if need_dyp else None), (dw if need_dw else None)

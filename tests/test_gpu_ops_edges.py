@@ -150,3 +150,31 @@ def test_product_of_the_most_tiles():
         assert torch.equal(y[e:e + 1], moe.moe_gemm_mxfp4(a[e:e + 1], a_sf[e:e + 1], b[e], b_sf[e])), e
     assert not torch.isnan(y).any()
     done(b, b_sf, y)
+
+
+def test_gradients_without_the_pool_list():
+    T, K, W, R = 6, 2, 70, 20
+    say("gradients without row_src")
+    src_row = (torch.randperm(R, device="cuda")[:T * K]).int()
+    src_row[3] = -1
+    row_src = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    for f, r in enumerate(src_row.tolist()):
+        if r >= 0:
+            row_src[r] = f
+    dy, yp, w = torch.randn(T, W, device="cuda"), torch.randn(R, W, device="cuda"), torch.rand(T, K, device="cuda")
+    want, dw = moe.moe_unpermute_bwd(dy, yp, row_src, src_row, None, w)
+    before = torch.randn(R, W, device="cuda")
+    want = torch.where((row_src >= 0)[:, None], want, before)        # the padding stays
+    for p in (yp, None):                                             # the pool's rows by yp, or by dyp
+        got, dw2 = moe.moe_unpermute_bwd(dy, p, None, src_row, None, w, dyp=before.clone(), need_dw=p is not None)
+        assert torch.equal(got, want) and (dw2 is None if p is None else torch.equal(dw2, dw))
+    none, dw2 = moe.moe_unpermute_bwd(dy, yp, None, src_row, None, w, need_dyp=False)
+    assert none is None and torch.equal(dw2, dw)
+    new, _ = moe.moe_unpermute_bwd(dy, yp, None, src_row, None, w)
+    assert torch.equal(new[row_src >= 0], want[row_src >= 0])
+    for bad in (lambda: moe.moe_unpermute_bwd(dy, None, row_src, src_row, None, w),
+                lambda: moe.moe_unpermute_bwd(dy, None, None, src_row, None, w, need_dw=False),
+                lambda: moe.moe_unpermute_bwd(dy, yp, None, src_row, None, w, dyp=before[1:].clone()),
+                lambda: moe.moe_unpermute_bwd(dy, yp[0], None, src_row, None, w)):
+        with pytest.raises(ValueError):
+            bad()
