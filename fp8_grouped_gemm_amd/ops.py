@@ -6,7 +6,11 @@ One function per entry point.  Tensors are checked here (type, shape, layout,
 device), before the library's own checks; outputs are allocated where none
 is passed, on the stream the call runs on.  Matrices of bf16, f16 or f32 rows
 may have a row stride; everything else is densely packed.  The functions take
-no part in autograd: the gradients are entry points of their own.
+no part in autograd: the gradients are entry points of their own.  So a call
+whose gradient would be lost is refused (grad mode on, and a float tensor of a
+permutation or an output requires grad): make it under torch.no_grad() or in an
+autograd.Function, whose backward calls the gradient's entry point.
+Quantisation, whose codes have no gradient, takes such an input.
 """
 import ctypes
 
@@ -87,8 +91,17 @@ def _elsewhere(fn, t, stream, *args, **kw):
     return out
 
 
-def _rows(t, name, dev, dtype, rows, width):
-    """Checks a [rows, width] matrix of rows; returns its row stride in elements."""
+def _lost(name):
+    """Refuses a tensor that requires grad, with grad mode on."""
+    raise ValueError(f"{name}: requires grad, and the call would record no graph (make it under "
+                     "torch.no_grad(), or in an autograd.Function with the gradient's entry point)")
+
+
+def _rows(t, name, dev, dtype, rows, width, codes=False):
+    """Checks a [rows, width] matrix of rows; returns its row stride in elements.
+    codes: the call's results are codes, which have no gradient."""
+    if t.requires_grad and not codes and torch.is_grad_enabled():
+        _lost(name)
     if t.dtype is not dtype or t.shape != (rows, width) or t.get_device() != dev:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
                          f"{(rows, width)} on device {dev}")
@@ -136,6 +149,15 @@ def _slots(src_row, num_tokens, dev):
     if num_tokens < 0 or (n % num_tokens or n == 0 if num_tokens else n):
         raise ValueError(f"src_row: {n} slots for {num_tokens} tokens")
     return _dense(src_row, "src_row", dev, torch.int32, n), n // num_tokens if num_tokens else 1
+
+
+def _weights(topk_w, dev, n):
+    """Checks topk_w (n elements, or None: all 1); returns its address."""
+    if topk_w is None:
+        return None
+    if topk_w.requires_grad and torch.is_grad_enabled():
+        _lost("topk_w")
+    return _dense(topk_w, "topk_w", dev, torch.float32, n)
 
 
 def _used(offsets, dev):
@@ -198,7 +220,7 @@ def moe_unpermute(yp, src_row, num_tokens, topk_w=None, out=None, stream=None):
         out = torch.empty(num_tokens, W, dtype=yp.dtype, device=yp.device)
     _check(ops_lib().moe_unpermute(
         num_tokens, K, R, W, dt, yp.data_ptr(), _rows(yp, "yp", dev, yp.dtype, R, W), src,
-        None if topk_w is None else _dense(topk_w, "topk_w", dev, torch.float32, num_tokens * K),
+        _weights(topk_w, dev, num_tokens * K),
         out.data_ptr(), _rows(out, "out", dev, yp.dtype, num_tokens, W), _raw_stream(dev)),
         "moe_unpermute")
     return out
@@ -235,6 +257,8 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
             # (no tokens: src_row is empty and only topk_w knows the slots per token)
             k = topk_w.shape[1] if T == 0 and topk_w is not None and topk_w.dim() == 2 else K
             dw = torch.empty(T, k, dtype=torch.float32, device=dy.device)
+        elif dw.requires_grad and torch.is_grad_enabled():
+            _lost("dw")
         dw_at = _dense(dw, "dw", dev, torch.float32, T * K)
     if need_dyp:
         if dyp is None:
@@ -244,7 +268,7 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
         T, K, R, W, dt, dy.data_ptr(), _rows(dy, "dy", dev, dy.dtype, T, W), yp_at, yp_ld,
         None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), src,
         _used(offsets, dev),
-        None if topk_w is None else _dense(topk_w, "topk_w", dev, torch.float32, T * K),
+        _weights(topk_w, dev, T * K),
         dyp_at, dyp_ld, dw_at, _raw_stream(dev)), "moe_unpermute_bwd")
     return (dyp if need_dyp else None), (dw if need_dw else None)
 
@@ -261,7 +285,7 @@ def moe_quantize_mxfp4(x, codes=None, sf=None, stream=None):
     if sf is None:
         sf = torch.empty(M, C // 32, dtype=u8, device=x.device)
     _check(ops_lib().moe_quantize_mxfp4(
-        M, C, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, M, C),
+        M, C, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, M, C, codes=True),
         _dense(codes, "codes", dev, u8, (M, C // 2)), _dense(sf, "sf", dev, u8, (M, C // 32)),
         _raw_stream(dev)), "moe_quantize_mxfp4")
     return codes, sf

@@ -178,3 +178,58 @@ def test_gradients_without_the_pool_list():
                 lambda: moe.moe_unpermute_bwd(dy, yp[0], None, src_row, None, w)):
         with pytest.raises(ValueError):
             bad()
+
+
+class Permute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, row_src, src_row, offsets):
+        ctx.lists, ctx.tokens = src_row, x.shape[0]
+        return moe.moe_permute(x, row_src, src_row, offsets)
+
+    @staticmethod
+    def backward(ctx, dxp):
+        return moe.moe_permute_bwd(dxp, ctx.lists, ctx.tokens), None, None, None
+
+
+class Unpermute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, yp, w, row_src, src_row, offsets):
+        ctx.lists = row_src, src_row, offsets
+        ctx.save_for_backward(yp, w)
+        return moe.moe_unpermute(yp, src_row, w.shape[0], w)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return *moe.moe_unpermute_bwd(dy, ctx.saved_tensors[0], *ctx.lists, ctx.saved_tensors[1]), None, None, None
+
+
+def test_gradients_are_not_lost_silently():
+    say("tensors that require grad")
+    T, W = 4, 32
+    i, offsets = torch.arange(T, dtype=torch.int32, device="cuda"), ints(0, T)
+    leaf = lambda *s: torch.randn(*s, device="cuda", requires_grad=True)
+    x, w, plain, one = leaf(T, W), leaf(T, 1), torch.randn(T, W, device="cuda"), torch.ones(T, 1, device="cuda")
+    codes, sf = moe.moe_quantize_mxfp4(x)                     # codes have no gradient
+    calls = [lambda: moe.moe_permute(x, i, i, offsets), lambda: moe.moe_permute(plain, i, i, offsets, out=x),
+             lambda: moe.moe_permute_bwd(x, i, T), lambda: moe.moe_permute_bwd(plain, i, T, out=x),
+             lambda: moe.moe_unpermute(x, i, T), lambda: moe.moe_unpermute(plain, i, T, w),
+             lambda: moe.moe_unpermute(plain, i, T, one, out=x),
+             lambda: moe.moe_unpermute_bwd(x, plain, i, i, offsets),
+             lambda: moe.moe_unpermute_bwd(plain, x, i, i, offsets),
+             lambda: moe.moe_unpermute_bwd(plain, plain, i, i, offsets, w),
+             lambda: moe.moe_unpermute_bwd(plain, plain, i, i, offsets, dyp=x),
+             lambda: moe.moe_unpermute_bwd(plain, plain, i, i, offsets, dw=w),
+             lambda: moe.moe_dequantize_mxfp4(codes, sf, torch.float32, out=x),
+             lambda: moe.moe_gemm_mxfp4(codes, sf, codes, sf, out=leaf(T, T))]
+    for n, f in enumerate(calls):
+        with pytest.raises(ValueError, match="requires grad"):
+            f()
+        if n in (0, 2, 4, 5, 9):
+            with torch.no_grad():                             # without grad mode they run
+                f()
+    # in autograd.Functions: rows, weighted, there and back
+    y = Unpermute.apply(Permute.apply(x, i, i, offsets), w, i, i, offsets)
+    dx, dw = torch.autograd.grad(y, (x, w), plain)
+    assert torch.equal(dx, plain * w)
+    terms = plain.double() * x.detach().double()              # a lane's products, then 6 levels of a tree
+    assert torch.all((dw[:, 0] - terms.sum(1)).abs() <= (W / 64 + 14) * 2.0 ** -24 * terms.abs().sum(1))
