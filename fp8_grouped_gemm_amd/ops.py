@@ -91,6 +91,11 @@ def _elsewhere(fn, t, stream, *args, **kw):
     return out
 
 
+# Tells autograd that the library wrote a caller's tensors: what it saved of them
+# is then refused in a backward pass, as after torch's own in-place writes.
+_wrote = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
 def _lost(name):
     """Refuses a tensor that requires grad, with grad mode on."""
     raise ValueError(f"{name}: requires grad, and the call would record no graph (make it under "
@@ -182,12 +187,15 @@ def moe_permute(x, row_src, src_row, offsets, out=None, stream=None):
     src, K = _slots(src_row, T, dev)
     R = row_src.numel()
     _int32("row_src", R)
+    given = out
     if out is None:
         out = torch.empty(R, W, dtype=x.dtype, device=x.device)
     _check(ops_lib().moe_permute(
         T, K, R, W, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, T, W),
         _dense(row_src, "row_src", dev, torch.int32, R), src, _used(offsets, dev),
         out.data_ptr(), _rows(out, "out", dev, x.dtype, R, W), _raw_stream(dev)), "moe_permute")
+    if given is not None:
+        _wrote((given,))
     return out
 
 
@@ -199,12 +207,15 @@ def moe_permute_bwd(dxp, src_row, num_tokens, out=None, stream=None):
     dev = dxp.get_device()
     dt, R, W = _matrix(dxp, "dxp", _DTYPES)
     src, K = _slots(src_row, num_tokens, dev)
+    given = out
     if out is None:
         out = torch.empty(num_tokens, W, dtype=dxp.dtype, device=dxp.device)
     _check(ops_lib().moe_permute_bwd(
         num_tokens, K, R, W, dt, dxp.data_ptr(), _rows(dxp, "dxp", dev, dxp.dtype, R, W), src,
         out.data_ptr(), _rows(out, "out", dev, dxp.dtype, num_tokens, W), _raw_stream(dev)),
         "moe_permute_bwd")
+    if given is not None:
+        _wrote((given,))
     return out
 
 
@@ -216,6 +227,7 @@ def moe_unpermute(yp, src_row, num_tokens, topk_w=None, out=None, stream=None):
     dev = yp.get_device()
     dt, R, W = _matrix(yp, "yp", _DTYPES)
     src, K = _slots(src_row, num_tokens, dev)
+    given = out
     if out is None:
         out = torch.empty(num_tokens, W, dtype=yp.dtype, device=yp.device)
     _check(ops_lib().moe_unpermute(
@@ -223,6 +235,8 @@ def moe_unpermute(yp, src_row, num_tokens, topk_w=None, out=None, stream=None):
         _weights(topk_w, dev, num_tokens * K),
         out.data_ptr(), _rows(out, "out", dev, yp.dtype, num_tokens, W), _raw_stream(dev)),
         "moe_unpermute")
+    if given is not None:
+        _wrote((given,))
     return out
 
 
@@ -249,6 +263,7 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
         raise ValueError("none of row_src, yp and dyp, which the pool's rows are known by")
     R = row_src.numel() if row_src is not None else pool.shape[0] if pool.dim() else 0
     _int32("row_src", R)
+    given = tuple(t for t, need in ((dyp, need_dyp), (dw, need_dw)) if need and t is not None)
     yp_at = dyp_at = dw_at = None
     yp_ld = dyp_ld = 0
     if need_dw:
@@ -270,6 +285,8 @@ def moe_unpermute_bwd(dy, yp, row_src, src_row, offsets, topk_w=None, dyp=None, 
         _used(offsets, dev),
         _weights(topk_w, dev, T * K),
         dyp_at, dyp_ld, dw_at, _raw_stream(dev)), "moe_unpermute_bwd")
+    if given:
+        _wrote(given)
     return (dyp if need_dyp else None), (dw if need_dw else None)
 
 
@@ -280,6 +297,7 @@ def moe_quantize_mxfp4(x, codes=None, sf=None, stream=None):
         return _elsewhere(moe_quantize_mxfp4, x, stream, x, codes, sf)
     dev, u8 = x.get_device(), torch.uint8
     dt, M, C = _matrix(x, "x", _DTYPES)
+    given = tuple(t for t in (codes, sf) if t is not None)
     if codes is None:
         codes = torch.empty(M, C // 2, dtype=u8, device=x.device)
     if sf is None:
@@ -288,6 +306,8 @@ def moe_quantize_mxfp4(x, codes=None, sf=None, stream=None):
         M, C, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, M, C, codes=True),
         _dense(codes, "codes", dev, u8, (M, C // 2)), _dense(sf, "sf", dev, u8, (M, C // 32)),
         _raw_stream(dev)), "moe_quantize_mxfp4")
+    if given:
+        _wrote(given)
     return codes, sf
 
 
@@ -300,12 +320,15 @@ def moe_dequantize_mxfp4(codes, sf, dtype=torch.bfloat16, out=None, stream=None)
         raise ValueError(f"codes: shape {tuple(codes.shape)}; dtype {dtype}")
     M, C = codes.shape[0], 2 * codes.shape[1]
     _int32("codes", max(M, C))
+    given = out
     if out is None:
         out = torch.empty(M, C, dtype=dtype, device=codes.device)
     _check(ops_lib().moe_dequantize_mxfp4(
         M, C, _DTYPES[dtype], _dense(codes, "codes", dev, u8, (M, C // 2)),
         _dense(sf, "sf", dev, u8, (M, C // 32)), out.data_ptr(),
         _rows(out, "out", dev, dtype, M, C), _raw_stream(dev)), "moe_dequantize_mxfp4")
+    if given is not None:
+        _wrote((given,))
     return out
 
 
@@ -335,6 +358,7 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
         dtype = torch.bfloat16 if out is None else out.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"dtype {dtype}")
+    given = out
     if out is None:
         out = torch.empty(R, N, dtype=dtype, device=a.device)
     _check(ops_lib().moe_gemm_mxfp4(
@@ -344,6 +368,8 @@ def moe_gemm_mxfp4(a, a_sf, b, b_sf, offsets=None, counts=None, dtype=None, out=
         None if offsets is None else _dense(offsets, "offsets", dev, i32, E + 1),
         None if counts is None else _dense(counts, "counts", dev, i32, E), slots,
         out.data_ptr(), _rows(out, "out", dev, dtype, R, N), _raw_stream(dev)), "moe_gemm_mxfp4")
+    if given is not None:
+        _wrote((given,))
     return out
 
 

@@ -233,3 +233,37 @@ def test_gradients_are_not_lost_silently():
     assert torch.equal(dx, plain * w)
     terms = plain.double() * x.detach().double()              # a lane's products, then 6 levels of a tree
     assert torch.all((dw[:, 0] - terms.sum(1)).abs() <= (W / 64 + 14) * 2.0 ** -24 * terms.abs().sum(1))
+
+
+def test_autograd_sees_writes_into_given_outputs():
+    # a tensor that a graph saved and a call overwrote is refused in the backward pass
+    say("outputs that autograd saved")
+    T, W = 4, 32
+    i, offsets = torch.arange(T, dtype=torch.int32, device="cuda"), ints(0, T)
+    x, w = torch.randn(T, W, device="cuda"), torch.rand(T, 1, device="cuda")
+    codes, sf = moe.moe_quantize_mxfp4(x)
+    calls = [lambda o: moe.moe_permute(x, i, i, offsets, out=o), lambda o: moe.moe_permute_bwd(x, i, T, out=o),
+             lambda o: moe.moe_unpermute(x, i, T, w, out=o),
+             lambda o: moe.moe_unpermute_bwd(x, x, i, i, offsets, w, dyp=o),
+             lambda o: moe.moe_unpermute_bwd(x, x, i, i, offsets, w, dw=o),
+             lambda o: moe.moe_dequantize_mxfp4(codes, sf, torch.float32, out=o),
+             lambda o: moe.moe_gemm_mxfp4(codes, sf, torch.cat([codes] * 8), torch.cat([sf] * 8), out=o)]
+    for n, f in enumerate(calls):
+        saved = torch.randn(T, 1 if n == 4 else W, device="cuda")
+        y = (saved * torch.randn_like(saved).requires_grad_()).sum()
+        f(saved)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    for given in (dict(codes=codes), dict(sf=sf), dict(codes=codes, sf=sf)):
+        before = {k: v._version for k, v in given.items()}
+        moe.moe_quantize_mxfp4(x, **given)
+        assert all(v._version > before[k] for k, v in given.items())
+    # a call that is refused, and one that writes nothing given, leave them
+    before = x._version
+    with pytest.raises(moe.MoEError):
+        moe.moe_permute(x, i, i, offsets, out=x)
+    moe.moe_permute(x, i, i, offsets)
+    moe.moe_unpermute_bwd(x, x, i, i, offsets, w, dyp=x, need_dyp=False)
+    assert x._version == before
+    with torch.inference_mode():                              # tensors without a version
+        moe.moe_permute(x, i, i, offsets, out=torch.empty(T, W, device="cuda"))
