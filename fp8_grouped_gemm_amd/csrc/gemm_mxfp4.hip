@@ -641,13 +641,31 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s)
 //   12288 x 4096 x 4096 (32)  2469   2028    492     326     317    204    170
 // A call that reads b once, and more of it than the L2s hold twice over
 // (streams_b), takes its tile from the last three kernels, whose copies of b
-// are nontemporal (32 x 128 with two and three buffers, 128^2); us:
+// are nontemporal (32 x 128 with two and three buffers, 128^2), and of the
+// others the few-rows ones; us:
 //   rows x n x k (experts)   cached 32x128   128^2   nt 32x128, 2   3   128^2
 //   32 x 4096 x 4096 (32)             31.3    46.0         29.3   35.5   45.1
 //   256 x 4096 x 4096 (32)            63.6    61.1         57.9   49.3   57.3
 //   768 x 4096 x 4096 (32)            63.4    64.1         61.4   64.2   59.6
 //   1536 x 4096 x 4096 (32)           85.8    76.6         94.1   95.0   70.5
 //   2048 x 4096 x 4096 (dense)        48.1    26.4         69.4   68.9   28.7
+// The two sides of streams_b's limits, the choice among either set, over 32
+// experts of 4096 columns with ROWS each, weights that no cache holds, us:
+//   b, ROWS          1       12       24       48       96      128      192      256
+//    40 MB    9.8 10.7  22 17    18 19    24 23    31 31    39 37    42 45    44 55
+//    66 MB   12.5 14.5  35 30    27 31    29 33    51 44    52 46    55 58    58 71
+//   128 MB   16.5 14.6  39 28.5  34 34    38 38    49 49    66 52    66 65    71 81
+//   256 MB   34   30    62 50    63 57    76 63    87 85    93 92   117 128  122 155
+// (the same 66 MB in every call, which the last-level cache then keeps: 24 rows 22 and
+// 29).  Between 32 and 128 rows an expert the two differ by the tile they lead to.
+// A dense call that streams has few tiles, and of the smaller cached ones a
+// whole round may run where the nontemporal ones leave half the units idle, so
+// those stay in the choice while they fit one round.  us, without and with
+// them: 16384 columns x 9216, 1 row 24.7 and 20.5, 32 rows 26.8 and 20.8, 96 rows 40.3
+// and 28.0; 12288 x 16384, 96 rows 66.2 and 42.7; 32768 x 8192, 64 rows 39.9 and 35.2.
+// Past one round they lose: 131072 x 2048, 1 row 25.6 and 32.4.  Over 105 such
+// calls (8192 to 151936 columns, 1 to 128 rows) the choice is 2 % from the best of all
+// kernels (geometric mean; 12 % without them), 21 % at worst.
 struct Choice {
     int bm, bn, per_cu;
     double fix, step, fix1, step1;
@@ -685,10 +703,11 @@ int choose(int E, int R, int N, int K, bool grouped)
     int best = 0;
     double least = 0.0;
     for (int i = 0; i < kNumChoices; ++i) {
-        if (i >= 2 && (i >= 7) != once)
-            continue;
         const Choice& c = kChoices[i];
         const double tiles = row_tiles(E, R, grouped, c.bm) * ((N + c.bn - 1) / c.bn);
+        const bool one_round = !grouped && (i == 2 || i == 4) && tiles <= kUnits;
+        if (i >= 2 && (i >= 7) != once && !(once && one_round))
+            continue;
         const double us = tiles <= kUnits ? c.fix1 + c.step1 * steps
                                           : std::ceil(tiles / (kUnits * c.per_cu)) * (c.fix + c.step * steps);
         if (i == 0 || us < least) {
