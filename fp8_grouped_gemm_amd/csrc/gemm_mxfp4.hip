@@ -287,15 +287,19 @@ __global__ __launch_bounds__(64 * WV) void mxfp4_rows(MxGemmArgs a, int col_tile
 // register for its four steps (lane group g takes codes 2 s + g, step s byte
 // s).  Codes past the end of K are 127, scale 1.
 //
-// 256 x 256 tiles at 8192 x 8192 x 7168: 233 to 239 us, 4.1 PFLOP/s.  Power bounds
-// them: the matrix cores alone sustain 6.2 PFLOP/s on random codes (9.2 on
-// zeros, where this call takes 190 us), and here they are busy half the cycles
-// at the clock that leaves.  Measured and not kept, us: four waves of 128 x 128
-// (297 against 280 on uniform codes), 64 x 128 per wave (285), copies spread over
-// three steps (290), raised wave priority (291), workgroups that walk tiles and
-// copy the next one's first stages early (288).  Tiles between the ones kept: 192 x 256
-// 317 here and 203 for 196 at 12288 rows over 32 experts of 4096 x 4096 (112 for 118 at
-// 6144), 128 x 256 395 and 241 (24.3 for 26.0 at 2048 x 4096 x 4096).
+// 256 x 256 tiles at 8192 x 8192 x 7168: 233 us on Gaussian rows, 236 on uniform
+// codes (4.1 PFLOP/s), 172 on zeros, the same inputs in every call.  Two things
+// bound them.  The pipeline: 403 thousand cycles whatever the data, of which the
+// matrix cores work 229 (57 %; other inputs in every call: 460 thousand, 50 %; LDS is
+// active 31 %; what the rest waits for has not been told apart).  And power, which sets the
+// clock: 2.24 GHz on zeros, 1.72 and 1.63 on the others.  (The matrix cores alone,
+// never idle, sustain 6.2 PFLOP/s on random codes, 155 us, and 9.2 on zeros, 105 us.)
+// Measured and not kept, us, uniform codes, when the form kept took 276 to 284: four
+// waves of 128 x 128 297, 64 x 128 per wave 285, copies spread over three steps 290,
+// raised wave priority 291, workgroups that walk tiles and copy the next one's
+// first stages early 288.  Tiles between the ones kept, as then: 192 x 256 317 here and
+// 203 for 196 at 12288 rows over 32 experts of 4096 x 4096 (112 for 118 at 6144), 128 x 256
+// 395 and 241 (24.3 for 26.0 at 2048 x 4096 x 4096).
 constexpr int kCodeStages = 4;  // stages per load of scale codes
 
 template <class T, int WM, int WN, int MI, int NI, int NBUF>
@@ -542,7 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mxfp4_tile(MxGemmArgs a, int col
     const int c = col0 + wn * NI * 32 + (lane % PIECES) * T::VEC;
     // whole aligned pieces bypass the caches: y is not read here, and what a
     // tile shares in its L2 stays (2048 x 4096 x 4096: 26.6 us cached, 25.1;
-    // 8192 x 8192 x 7168: 278, 273; unaligned ones would be split)
+    // 8192 x 8192 x 7168, uniform codes, then: 278, 273; unaligned ones would be split)
     const bool nt = (reinterpret_cast<uintptr_t>(a.y) | a.y_ld) % 16 == 0;
 #pragma unroll
     for (int m = 0; m < MI; ++m) {

@@ -1,7 +1,8 @@
 // Rows to and from microscaled 4-bit floating point (include/moe_ops.h:
 // moe_quantize_mxfp4, moe_dequantize_mxfp4): per 32 columns
 //   sf = the smallest power of two >= max(amax, 1e-10) / 6,  q = e2m1(v / sf),
-// the library's rule for e2m1 weights.  amax / 6 needs no division: with
+// the library's rule for e2m1 weights (other MX quantisers take 2^(floor(log2 amax) - 2) and
+// let values past 6 saturate).  amax / 6 needs no division: with
 // amax = 1.m 2^e, the power of two is 2^(e - 2) if 1.m <= 1.5 and
 // 2^(e - 1) otherwise.  v / sf is exact (a power of two), so each value
 // rounds once, in v_cvt_scalef32_pk_fp4_f32 (nearest, ties to even).
@@ -44,8 +45,14 @@ int row_threads(int n)
 }
 
 // Whether the values stream past the caches (nontemporal): aligned 16-byte
-// pieces, and more than the eight L2s hold twice over (65536 x 4096 bf16 there
-// and back: 315 us without, 257 with).
+// pieces, and more than the eight L2s hold twice over.  Cached and streamed, us,
+// rows of 4096 bf16, other inputs in every call:
+//   values   quantise  dequantise  there and back  written, quantised  dequantised, read
+//    32 MB   10.8 10.4 13.8  9.8   23 21           22.5 23.1           25 27
+//    64 MB   19.3 18.3 23.6 22.3   40 36           40 39               44 48
+//   128 MB   35   34   43   42     76 66           72 71               86 89
+//   402 MB   98   97  128  124    233 198         240 218             271 264
+// A caller that reads the values next pays for small ones, so those stay cached.
 bool streams(const MxQuantArgs& a, int size)
 {
     return (int64_t)a.rows * a.cols * size > (INT64_C(64) << 20) &&
@@ -83,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void quantize_mxfp4(MxQuantArgs a, int tp
     uint32_t code = 0xFFu, q = 0;
     if (m < 0x7F800000u) {
         const uint32_t u = max(m, __float_as_uint(1e-10f));
-        code = (u >> 23) - 2 + ((u & 0x7FFFFFu) > 0x400000u);  // 91 .. 253
+        code = (u >> 23) - 2 + ((u & 0x7FFFFFu) > 0x400000u);  // 92 .. 253
         const float sf = __uint_as_float(code << 23);
         q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], sf, 0);
         q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], sf, 1);

@@ -49,12 +49,23 @@ __device__ __forceinline__ void clear_padding(const RowsArgs& a, int r0, int row
 
 // Whether a call's pool rows stream past the caches (nontemporal accesses):
 // whole aligned 16-byte pieces, and more of them than the eight L2s hold
-// twice over.  Measured cached and streamed, us: permute 8192 x 6 x 7168 bf16
-// 175 and 145, its gradient 4096 x 8 x 4096 f32 109 and 92, unpermute 173 and
-// 161, its gradient 4096 x 8 x 4096 117 and 110; but rows of 4097 bf16
-// (unaligned) 52 and 57, the gradient at 512 x 8 x 4096 (34 MB) 15 and 19.  The
-// token rows stay cached: several workgroups read them (permute 145, 176
-// streamed).
+// twice over.  Measured cached and streamed, us, other inputs in every call:
+// permute 8192 x 6 x 7168 bf16 174 and 173 (146 where the last-level cache still holds
+// the token rows; 260 and 259, 229, with the padding of 128-row segments), its
+// gradient 4096 x 8 x 4096 f32 119 and 99, unpermute 8192 x 6 x 7168 172 and 160, its
+// gradient 4096 x 8 x 4096 128 and 123; rows of 4097 bf16 (unaligned) 52 and 57.
+// Around the limit, top-8 of 4096 bf16:
+//   pool   permute    gradient   unpermute's   permute +    permute +
+//                                gradient      unpermute    quantise
+//    32 MB  9.0  8.4  12.8 12.5  19.5 18.4     18.4 19.7    18.4 18.5
+//    64 MB 16.1 14.7  17.1 16.9  33.8 31.7     28.6 31.2    30.1 33.6
+//   128 MB 30   27    32   31    79   68       60   57      53   62
+//   192 MB 45   40    46   44    90   87       78   82      81   92
+//   402 MB 94   81    97   87   184  178      210  165     174  187
+// Streaming is the faster by itself, but the call that reads the pool next pays for it
+// while the last-level cache could hold the pool; small pools, which are read
+// soon, stay cached.  The token rows stay cached too: several workgroups
+// read them (permute 145, 176 streamed, the same inputs in every call).
 bool streams(const RowsArgs& a, const void* pool, int64_t pool_ld, int size)
 {
     const int64_t row = (int64_t)a.width * size;

@@ -104,7 +104,10 @@ int moe_unpermute_bwd(int32_t num_tokens, int32_t top_k, int32_t pool_rows, int3
 /*
  * Rows to microscaled 4-bit floating point, 32 columns per block:
  *   sf = the smallest power of two >= max(amax, 1e-10) / 6, q = e2m1(v / sf)
- * rounded to nearest, ties to the even code (no value saturates).
+ * rounded to nearest, ties to the even code (no value saturates).  This is the
+ * library's rule for e2m1 weights; the OCP MX specification's conversion takes
+ * sf = 2^(floor(log2(amax)) - 2) instead and saturates what then exceeds 6.  A block
+ * whose amax is 2^-37 or less becomes zeros (the floor of 1e-10 keeps sf >= 2^-35).
  *   x      [rows, cols] bf16, f16 or f32, row stride x_ld; cols % 32 == 0
  *   codes  uint8 [rows, cols/2]   element k of a row in byte k/2, even k in the low nibble
  *   sf     uint8 [rows, cols/32]  UE8M0: 2^(code - 127)
