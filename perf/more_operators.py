@@ -87,12 +87,13 @@ def draw(rng):
         top_groups = rng.randint(1, groups)
         top_k = rng.randint(1, min(12, experts // groups * top_groups))
         tokens = max(1, min(_log(rng, 1, 32768), MOST_LOGITS // 2 // experts))
-        # (a router that sums a group's best has a bias: without one sigmoid(x) + sigmoid(-x) would tie)
+        # (a router that sums a group's best has a bias: without one sigmoid(x) + sigmoid(-x) would tie;
+        # one weight alone is not renormalised: it would be 1, and its gradient nothing but roundings)
         group_top = min(rng.choice([1, 2]), experts // groups)
         return dict(op=op, dtype=dtype, tokens=tokens, experts=experts, top_k=top_k,
                     score=rng.choice(["softmax", "sigmoid"]), bias=group_top == 2 or rng.random() < 0.5,
                     groups=groups, top_groups=top_groups, group_top=group_top,
-                    renorm=rng.random() < 0.7, masked=rng.choice([0.0, 0.0, 0.1, 0.5]))
+                    renorm=top_k > 1 and rng.random() < 0.7, masked=rng.choice([0.0, 0.0, 0.1, 0.5]))
     if op in ("norm", "norm_grad"):
         sf = rng.choice(["", "f32", "ue8m0"]) if op == "norm" else ""
         width = BLOCK[sf] * _log(rng, 1, 8192 // BLOCK[sf]) if sf else _log(rng, 16, 8192)
