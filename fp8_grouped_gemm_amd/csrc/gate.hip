@@ -1,0 +1,441 @@
+// The router's choice of experts and its gradient (include/moe_ops.h: moe_gate,
+// moe_gate_bwd).
+//   s = softmax(l) or sigmoid(l),  c = s + bias (without a bias: the order of l)
+//   the K largest c, of the best groups' experts;  w_j = scale s_j / (S + 1e-20), S = sum s_j
+// and with D = S + 1e-20, g = scale dw
+//   dp_j = (sum_i p_i (g_j - g_i) + 1e-20 g_j) / D^2,  q = sum_j dp_j p_j = 1e-20 sum g p / D^2
+//   softmax dl_e = s_e (dp_e - q),  sigmoid dl_e = dp_e s_e (1 - s_e)
+// (dp as a sum of differences: g_j - sum g p / D loses everything where one slot
+// holds all the weight; without renorm dp_j = g_j, q = sum g p).
+//
+// One wave per token, each lane a run of N adjacent experts in registers, so that the
+// lowest lane holding a maximum also holds the lowest id.  Values are compared as
+// integers in the order of the values (NaN on top, 0 for experts that cannot be
+// chosen), whose maximum over a wave is six instructions.
+#include "../../include/moe_ops.h"
+#include "ops_internal.h"
+#include "rows_device.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr float kTiny = 1e-20f;  // added to the chosen scores' sum
+
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane)
+{
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+__device__ __forceinline__ float lane_of(float v, int lane)
+{
+    return __uint_as_float(lane_of(__float_as_uint(v), lane));
+}
+
+// The maximum over the wave, in every lane (a scalar).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = max(v, row_perm_u<0xB1>(v));   // quad_perm [1,0,3,2]
+    v = max(v, row_perm_u<0x4E>(v));   // quad_perm [2,3,0,1]
+    v = max(v, row_perm_u<0x141>(v));  // row_half_mirror
+    v = max(v, row_perm_u<0x140>(v));  // row_mirror
+    return max(max(lane_of(v, 0), lane_of(v, 16)), max(lane_of(v, 32), lane_of(v, 48)));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += row_perm<0xB1>(v);
+    v += row_perm<0x4E>(v);
+    v += row_perm<0x141>(v);
+    v += row_perm<0x140>(v);
+    return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2)
+        v += __shfl_xor(v, x);
+    return v;
+}
+
+// Integers in the order of the values: -0 counts as 0, NaN as the largest, and
+// 0 is below every value's (-infinity is no choice and never asked for).
+__device__ __forceinline__ uint32_t order32(float v)
+{
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return v != v ? 0xFFFFFFFFu : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float from_order32(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ uint64_t order64(double v)
+{
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return v != v ? ~UINT64_C(0) : u ^ ((uint64_t)((int64_t)u >> 63) | UINT64_C(1) << 63);
+}
+
+__device__ __forceinline__ double from_order64(uint64_t k)
+{
+    return __longlong_as_double((long long)(k >> 63 ? k ^ UINT64_C(1) << 63 : ~k));
+}
+
+// A lane's N experts of a row of n, from e0 on; -infinity past the row.
+template <class E, int N>
+__device__ __forceinline__ void load_run(const char* row, int e0, int n, float* f)
+{
+    alignas(16) char raw[N * E::SIZE];
+    if (e0 + N <= n) {
+        __builtin_memcpy(raw, row + (int64_t)e0 * E::SIZE, N * E::SIZE);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            f[i] = E::load(raw + i * E::SIZE);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            f[i] = e0 + i < n ? E::load(row + (int64_t)(e0 + i) * E::SIZE) : -INFINITY;
+    }
+}
+
+template <class E, int N>
+__device__ __forceinline__ void store_run(char* row, int e0, int n, const float* f)
+{
+    if (e0 + N <= n) {
+        alignas(16) char raw[N * E::SIZE];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            E::store(raw + i * E::SIZE, f[i]);
+        __builtin_memcpy(row + (int64_t)e0 * E::SIZE, raw, N * E::SIZE);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e0 + i < n)
+                E::store(row + (int64_t)(e0 + i) * E::SIZE, f[i]);
+    }
+}
+
+// m and the sum of exp(l - m) over the row (m NaN with a NaN in the row).
+template <int N>
+__device__ __forceinline__ float softmax_sum(const float* l, float& m)
+{
+    uint32_t k = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        k = max(k, order32(l[i]));
+    m = from_order32(wave_max(k));
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        z += expf(l[i] - m);
+    return wave_sum(z);
+}
+
+__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+
+// The largest key of the wave: its lane (the lowest of equals); false if all keys are 0.
+template <bool WIDE>
+__device__ __forceinline__ bool wave_best(uint32_t hi, uint32_t lo, int& lane)
+{
+    const uint32_t top = wave_max(hi);
+    if (top == 0)
+        return false;
+    uint64_t who = __ballot(hi == top);
+    if (WIDE && (who & (who - 1))) {
+        const uint32_t low = wave_max(hi == top ? lo : 0u);
+        who = __ballot(hi == top && lo == low);
+    }
+    lane = __builtin_ctzll(who);
+    return true;
+}
+
+}  // namespace
+
+// WIDE: the choice, or the groups' sums, need the scores in 64 bits.  LDS: E keys
+// of 8 bytes per wave with groups.
+template <class E, int N, bool WIDE>
+__global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_size, unsigned magic)
+{
+    extern __shared__ uint64_t group_keys[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)workgroup() * kWaves + wave;
+    if (t >= a.T)
+        return;
+    int32_t* const idx = a.idx + t * a.K;
+    float* const w = a.w + t * a.K;
+    if (a.mask && !a.mask[t]) {
+        if (lane < a.K) {
+            idx[lane] = -1;
+            w[lane] = 0.f;
+        }
+        return;
+    }
+    const char* const row = a.logits + t * a.ld;
+    const int e0 = lane * N;
+    float l[N];
+    load_run<E, N>(row, e0, a.E, l);
+
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    float m = 0.f, z = 1.f;
+    if (softmax)
+        z = softmax_sum<N>(l, m);
+
+    // keys: the logits' order, or (WIDE) that of c in 64 bits
+    uint32_t hi[N], lo[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        hi[i] = l[i] == -INFINITY ? 0u : order32(l[i]);
+        lo[i] = 0;
+    }
+    if constexpr (WIDE) {
+        double c[N], zd = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            c[i] = exp(softmax ? (double)l[i] - (double)m : -(double)l[i]);
+        if (softmax) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                zd += c[i];
+            zd = wave_sum(zd);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double s = softmax ? c[i] / zd : 1.0 / (1.0 + c[i]);
+            const float b = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+            const bool on = l[i] != -INFINITY && b != -INFINITY;
+            const uint64_t k = on ? order64(s + (double)b) : 0;
+            hi[i] = (uint32_t)(k >> 32);
+            lo[i] = (uint32_t)k;
+        }
+    }
+
+    if (a.groups > 1) {
+        uint64_t* const keys = group_keys + wave * a.E;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e0 + i < a.E)
+                keys[e0 + i] = (uint64_t)hi[i] << 32 | lo[i];
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        // lane g sums group g's best: each pass finds the largest key behind the
+        // last one's (key descending, id ascending)
+        uint64_t group_key = 0;
+        if (lane < a.groups) {
+            const uint64_t* const of = keys + lane * group_size;
+            uint64_t last = ~UINT64_C(0);
+            int last_at = -1;
+            double sum = 0;
+            for (int p = 0; p < a.group_top; ++p) {
+                uint64_t best = 0;
+                int at = group_size;
+                int j = lane % group_size;  // (lanes start apart: their keys lie in different banks)
+                for (int n = 0; n < group_size; ++n) {
+                    const uint64_t k = of[j];
+                    const bool later = k < last || (k == last && j > last_at);
+                    if (later && (k > best || (k == best && j < at))) {
+                        best = k;
+                        at = j;
+                    }
+                    j = j + 1 == group_size ? 0 : j + 1;
+                }
+                if (best == 0)
+                    break;
+                if (WIDE)
+                    sum += from_order64(best);
+                else
+                    group_key = best;  // (group_top is 1)
+                last = best;
+                last_at = at;
+            }
+            if (WIDE && last_at >= 0)
+                group_key = order64(sum);
+        }
+        uint64_t kept = 0;
+        for (int p = 0; p < a.top_groups; ++p) {
+            int g;
+            if (!wave_best<true>((uint32_t)(group_key >> 32), (uint32_t)group_key, g))
+                break;
+            kept |= UINT64_C(1) << g;
+            if (lane == g)
+                group_key = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const unsigned g = (unsigned)(e0 + i) * magic >> 20;  // (e0 + i) / group_size
+            if (e0 + i >= a.E || !(kept >> (g & 63) & 1))
+                hi[i] = lo[i] = 0;
+            else if (WIDE && !a.bias && hi[i] != 0) {  // the groups are chosen: back to the logits' order
+                hi[i] = order32(l[i]);
+                lo[i] = 0;
+            }
+        }
+    }
+
+    // each lane its best expert; K times the wave's best, whose lane then looks for its next
+    int mine = -1;
+    uint32_t best_hi, best_lo;
+    int best_i;
+    const auto look = [&] {
+        best_hi = hi[0], best_lo = lo[0], best_i = 0;
+#pragma unroll
+        for (int i = 1; i < N; ++i)
+            if (hi[i] > best_hi || (WIDE && hi[i] == best_hi && lo[i] > best_lo))
+                best_hi = hi[i], best_lo = lo[i], best_i = i;
+    };
+    look();
+    for (int j = 0; j < a.K; ++j) {
+        int from;
+        if (!wave_best<WIDE>(best_hi, best_lo, from))
+            break;
+        const int i_from = (int)lane_of((uint32_t)best_i, from);
+        if (lane == j)
+            mine = from * N + i_from;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane == from && i == i_from)
+                hi[i] = lo[i] = 0;
+        look();
+    }
+
+    // lane j the weight of slot j
+    float s = 0.f;
+    if (mine >= 0) {
+        const float v = E::load(row + (int64_t)mine * E::SIZE);
+        s = softmax ? expf(v - m) / z : sigmoid(v);
+    }
+    if (a.renorm)
+        s = s / (wave_sum(s) + kTiny);
+    if (lane < a.K) {
+        idx[lane] = mine;
+        w[lane] = mine >= 0 ? a.scale * s : 0.f;
+    }
+}
+
+template <class E, int N>
+__global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)workgroup() * kWaves + wave;
+    if (t >= a.T)
+        return;
+    char* const out = a.dlogits + t * a.dlogits_ld;
+    const int e0 = lane * N;
+    int mine = lane < a.K ? a.idx[t * a.K + lane] : -1;
+    if (mine >= a.E)
+        mine = -1;
+    float d[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        d[i] = 0.f;
+    const uint64_t slots = __ballot(mine >= 0);
+    if (slots != 0) {
+        const char* const row = a.logits + t * a.ld;
+        const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+        float l[N], m = 0.f, z = 1.f;
+        load_run<E, N>(row, e0, a.E, l);
+        if (softmax)
+            z = softmax_sum<N>(l, m);
+        float p = 0.f, g = 0.f;
+        if (mine >= 0) {
+            const float v = E::load(row + (int64_t)mine * E::SIZE);
+            p = softmax ? expf(v - m) / z : sigmoid(v);
+            g = a.scale * a.w[t * a.K + lane];
+        }
+        float dp = g, q = 0.f;
+        if (softmax || a.renorm)
+            q = wave_sum(g * p);
+        if (a.renorm) {
+            const float total = wave_sum(p) + kTiny;
+            dp = kTiny * g;
+            for (uint64_t left = slots; left; left &= left - 1) {
+                const int i = __builtin_ctzll(left);
+                dp = __builtin_fmaf(lane_of(p, i), g - lane_of(g, i), dp);
+            }
+            dp = dp / total / total;
+            q = kTiny * q / total / total;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            d[i] = softmax ? -q : 0.f;
+        for (uint64_t left = slots; left; left &= left - 1) {
+            const int j = __builtin_ctzll(left);
+            const int at = (int)lane_of((uint32_t)mine, j) - e0;
+            const float add = lane_of(dp, j);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                d[i] += at == i ? add : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (softmax) {
+                d[i] *= expf(l[i] - m) / z;
+            } else {  // s (1 - s) without 1 - s, which loses the small ones
+                const float e = expf(-fabsf(l[i]));
+                d[i] *= e / ((1.f + e) * (1.f + e));
+            }
+        }
+    }
+    store_run<E, N>(out, e0, a.E, d);
+}
+
+// ------------------------------------------------------------ launchers
+
+namespace {
+
+template <class E, int N>
+hipError_t launch(const GateArgs& a, bool back, hipStream_t s)
+{
+    const dim3 grid = grid_of(((int64_t)a.T + kWaves - 1) / kWaves), block(kThreads);
+    if (back) {
+        hipLaunchKernelGGL((gate_grad<E, N>), grid, block, 0, s, a);
+        return hipGetLastError();
+    }
+    const int size = a.E / a.groups;
+    // e / size for e < 1024 and size <= 1024: the error, e (magic - 2^20 / size) / 2^20, stays below 1 / size
+    const unsigned magic = ((1u << 20) + size - 1) / size;
+    const size_t lds = a.groups > 1 ? (size_t)kWaves * a.E * 8 : 0;
+    const bool wide = a.bias || (a.groups > 1 && a.group_top > 1);
+    const auto kernel = wide ? gate_choose<E, N, true> : gate_choose<E, N, false>;
+    hipLaunchKernelGGL(kernel, grid, block, lds, s, a, size, magic);
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t launch_run(const GateArgs& a, bool back, hipStream_t s)
+{
+    const int n = (a.E + 63) / 64;
+    if (n <= 1)
+        return launch<E, 1>(a, back, s);
+    if (n <= 2)
+        return launch<E, 2>(a, back, s);
+    if (n <= 4)
+        return launch<E, 4>(a, back, s);
+    if (n <= 6)
+        return launch<E, 6>(a, back, s);
+    if (n <= 8)
+        return launch<E, 8>(a, back, s);
+    return launch<E, 16>(a, back, s);
+}
+
+hipError_t launch_type(const GateArgs& a, bool back, hipStream_t s)
+{
+    switch (a.dtype) {
+    case MOE_DTYPE_BF16: return launch_run<Bf16>(a, back, s);
+    case MOE_DTYPE_F16: return launch_run<F16>(a, back, s);
+    case MOE_DTYPE_F32: return launch_run<F32>(a, back, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_gate(const GateArgs& a, hipStream_t s) { return launch_type(a, false, s); }
+
+hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t s) { return launch_type(a, true, s); }
+
+}  // namespace moe

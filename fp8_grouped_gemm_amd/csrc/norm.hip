@@ -1,0 +1,438 @@
+// Residual and root-mean-square norm of token rows, and the gradients
+// (include/moe_ops.h: moe_rms_norm, moe_rms_norm_bwd).
+//   z = round(x + residual),  rstd = (mean(z^2) + eps)^(-1/2),  y = z rstd w
+//   xh = z rstd,  g = dy w:  dx = rstd (g - xh mean(g xh)) + dz,  dw = sum over rows of dy xh
+//
+// Both move bytes: a row is read once and stays in registers between its sum and
+// its result (rows over kMaxResident columns are read a second time), eight columns
+// a thread and step, and y is quantised from the registers, where a block's threads
+// share its largest magnitude by lane swaps.  dw needs sums over rows: a workgroup
+// walks many rows with its columns' sums in registers, writes them to the workspace
+// once, and a second kernel adds those partial rows in a fixed order (no atomics).
+#include "../../include/moe_ops.h"
+#include "fp8_rows.h"
+#include "ops_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxResident = 16384;
+constexpr int kPartials = 512;       // most partial rows of dw
+constexpr int kColumnThreads = 256;
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2)
+        v += __shfl_xor(v, x);
+    return v;
+}
+
+// The sum over the TPR threads of a row; `red` is not written again before every
+// thread has passed another barrier.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red)
+{
+    v = wave_sum(v);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0)
+            red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i)
+            v += red[i];
+    }
+    return v;
+}
+
+template <class W>
+__device__ __forceinline__ void load_weight(const char* w, int col, int n, float* f)
+{
+    if (w) {
+        load8<W>(w + (int64_t)col * W::SIZE, n, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = 1.f;
+    }
+}
+
+// z of eight columns: x, or the rounded sum with the residual.
+template <class E>
+__device__ __forceinline__ void load_z(const NormArgs& a, int64_t row, int col, int n, float* z)
+{
+    load8<E>(a.x + row * a.x_ld + (int64_t)col * E::SIZE, n, z);
+    if (a.res) {
+        float r[8];
+        load8<E>(a.res + row * a.res_ld + (int64_t)col * E::SIZE, n, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] += r[i];
+        round8<E>(z);
+    }
+}
+
+// y of eight columns from z, to the outputs the call asks for.
+template <class E, class W>
+__device__ __forceinline__ void finish(const NormArgs& a, int64_t row, int col, int n, float rstd, float* z)
+{
+    if (n <= 0)
+        return;
+    float w[8];
+    load_weight<W>(a.weight, col, n, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        z[i] = z[i] * rstd * w[i];
+    if (a.y)
+        store8<E>(a.y + row * a.y_ld + (int64_t)col * E::SIZE, n, z);
+    if (a.codes) {
+        uint8_t* const codes = a.codes + row * a.width;
+        if (a.sf_format == MOE_SF_UE8M0_32)
+            store_codes<true>(z, col, codes, static_cast<char*>(a.sf) + row * (a.width / 32));
+        else
+            store_codes<false>(z, col, codes, static_cast<char*>(a.sf) + row * (a.width / 128) * 4);
+    }
+}
+
+__device__ __forceinline__ float rstd_of(float sum, const NormArgs& a)
+{
+    return 1.f / sqrtf(sum / (float)a.width + a.eps);
+}
+
+constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+}  // namespace
+
+// TPR threads per row, each with CH steps of eight columns.
+template <class E, class W, int TPR, int CH>
+__global__ __launch_bounds__(threads_of(TPR)) void norm_rows(NormArgs a)
+{
+    __shared__ float red[16];
+    const int at = threadIdx.x % TPR;
+    const int64_t row = (int64_t)workgroup() * (threads_of(TPR) / TPR) + threadIdx.x / TPR;
+    if (row >= a.rows)
+        return;
+    float z[CH][8], sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int col = (c * TPR + at) * 8;
+        load_z<E>(a, row, col, a.width - col, z[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int col = (c * TPR + at) * 8;
+        if (a.z)
+            store8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, a.width - col, z[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum = __builtin_fmaf(z[c][i], z[c][i], sum);
+    }
+    const float rstd = rstd_of(row_sum<TPR>(sum, red), a);
+    if (a.rstd && at == 0)
+        a.rstd[row] = rstd;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int col = (c * TPR + at) * 8;
+        finish<E, W>(a, row, col, a.width - col, rstd, z[c]);
+    }
+}
+
+// Rows that do not fit the registers: read again for the result.
+template <class E, class W>
+__global__ __launch_bounds__(1024) void norm_rows_wide(NormArgs a)
+{
+    __shared__ float red[16];
+    const int64_t row = workgroup();
+    if (row >= a.rows)
+        return;
+    float sum = 0.f;
+    for (int col = threadIdx.x * 8; col < a.width; col += 1024 * 8) {
+        const int n = a.width - col;
+        float z[8];
+        load_z<E>(a, row, col, n, z);
+        if (a.z)
+            store8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum = __builtin_fmaf(z[i], z[i], sum);
+    }
+    const float rstd = rstd_of(row_sum<1024>(sum, red), a);
+    if (a.rstd && threadIdx.x == 0)
+        a.rstd[row] = rstd;
+    for (int col = threadIdx.x * 8; col < a.width; col += 1024 * 8) {
+        const int n = a.width - col;
+        float z[8];
+        if (a.z)  // (x or the residual may be gone: z may stand on it)
+            load8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n, z);
+        else
+            load_z<E>(a, row, col, n, z);
+        finish<E, W>(a, row, col, n, rstd, z);
+    }
+}
+
+// dx of a row whose sum of g xh is known, eight columns.
+template <class E>
+__device__ __forceinline__ void store_dx(const NormArgs& a, int64_t row, int col, int n, float rstd, float c,
+                                         const float* g, const float* xh)
+{
+    float d[8];
+    if (a.res) {
+        load8<E>(a.res + row * a.res_ld + (int64_t)col * E::SIZE, n, d);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            d[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        d[i] = __builtin_fmaf(rstd, __builtin_fmaf(-xh[i], c, g[i]), d[i]);
+    store8<E>(a.y + row * a.y_ld + (int64_t)col * E::SIZE, n, d);
+}
+
+// A row group (a workgroup, or a wave where TPR is 64) takes rows in steps of the
+// number of groups and keeps its columns' sums for dw.
+template <class E, class W, int TPR, int CH, bool DX, bool DW>
+__global__ __launch_bounds__(threads_of(TPR)) void norm_grad(NormArgs a, int groups)
+{
+    __shared__ float red[2][16];
+    const int at = threadIdx.x % TPR;
+    const int group = blockIdx.x * (threads_of(TPR) / TPR) + threadIdx.x / TPR;
+    if (group >= groups)
+        return;
+    float acc[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[c][i] = 0.f;
+    int turn = 0;
+    for (int64_t row = group; row < a.rows; row += groups, turn ^= 1) {
+        const float rstd = a.rstd[row];
+        float g[CH][8], xh[CH][8], sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int col = (c * TPR + at) * 8, n = a.width - col;
+            load8<E>(a.x + row * a.x_ld + (int64_t)col * E::SIZE, n, g[c]);
+            load8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n, xh[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int col = (c * TPR + at) * 8;
+            float w[8];
+            if (DX)
+                load_weight<W>(a.weight, col, a.width - col, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xh[c][i] *= rstd;
+                if (DW)
+                    acc[c][i] = __builtin_fmaf(g[c][i], xh[c][i], acc[c][i]);
+                if (DX) {
+                    g[c][i] *= w[i];
+                    sum = __builtin_fmaf(g[c][i], xh[c][i], sum);
+                }
+            }
+        }
+        if (DX) {
+            const float mean = row_sum<TPR>(sum, red[turn]) / (float)a.width;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int col = (c * TPR + at) * 8;
+                if (col < a.width)
+                    store_dx<E>(a, row, col, a.width - col, rstd, mean, g[c], xh[c]);
+            }
+        }
+    }
+    if (DW) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int col = (c * TPR + at) * 8;
+            store8<F32>(reinterpret_cast<char*>(a.partial + (int64_t)group * a.width + col), a.width - col, acc[c]);
+        }
+    }
+}
+
+// dx of rows that do not fit the registers.
+template <class E, class W>
+__global__ __launch_bounds__(1024) void norm_dx_wide(NormArgs a)
+{
+    __shared__ float red[16];
+    const int64_t row = workgroup();
+    if (row >= a.rows)
+        return;
+    const float rstd = a.rstd[row];
+    const auto load = [&](int col, float* g, float* xh) {
+        const int n = a.width - col;
+        float w[8];
+        load8<E>(a.x + row * a.x_ld + (int64_t)col * E::SIZE, n, g);
+        load8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n, xh);
+        load_weight<W>(a.weight, col, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[i] *= w[i];
+            xh[i] *= rstd;
+        }
+    };
+    float sum = 0.f;
+    for (int col = threadIdx.x * 8; col < a.width; col += 1024 * 8) {
+        float g[8], xh[8];
+        load(col, g, xh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum = __builtin_fmaf(g[i], xh[i], sum);
+    }
+    const float mean = row_sum<1024>(sum, red) / (float)a.width;
+    for (int col = threadIdx.x * 8; col < a.width; col += 1024 * 8) {
+        float g[8], xh[8];
+        load(col, g, xh);
+        store_dx<E>(a, row, col, a.width - col, rstd, mean, g, xh);
+    }
+}
+
+// Partial rows of dw by columns, for rows that do not fit the registers: workgroup
+// (c, p) takes rows p, p + groups, ...
+template <class E>
+__global__ __launch_bounds__(kColumnThreads) void norm_dw_wide(NormArgs a, int groups, unsigned strips)
+{
+    const unsigned wg = workgroup(), p = wg / strips;
+    const int col = (int)((wg - p * strips) * kColumnThreads + threadIdx.x) * 8;
+    if (p >= (unsigned)groups || col >= a.width)
+        return;
+    const int n = a.width - col;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t row = p; row < a.rows; row += groups) {
+        const float rstd = a.rstd[row];
+        float g[8], z[8];
+        load8<E>(a.x + row * a.x_ld + (int64_t)col * E::SIZE, n, g);
+        load8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[i] = __builtin_fmaf(g[i], z[i] * rstd, acc[i]);
+    }
+    store8<F32>(reinterpret_cast<char*>(a.partial + (int64_t)p * a.width + col), n, acc);
+}
+
+// dw = sum of the partial rows: 64 columns a workgroup, 16 threads of four columns by 16
+// runs of rows, whose sums meet in LDS in ascending order.
+__global__ __launch_bounds__(256) void norm_dw_sum(const float* partial, int groups, int width, float* dw)
+{
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 15, run = threadIdx.x >> 4;
+    const int col = blockIdx.x * 64 + lane * 4, n = width - col;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = run; p < groups; p += 16) {
+        float v[4];
+        load_vec<F32>(reinterpret_cast<const char*>(partial + (int64_t)p * width + col), n, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] += v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        part[run][lane * 4 + i] = acc[i];
+    __syncthreads();
+    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < width) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            s += part[r][threadIdx.x];
+        dw[blockIdx.x * 64 + threadIdx.x] = s;
+    }
+}
+
+// ------------------------------------------------------------ launchers
+
+int norm_partials(int rows, int width) { return rows < kPartials ? rows : kPartials; }
+
+namespace {
+
+template <class E, class W, int TPR, int CH>
+hipError_t launch_rows(const NormArgs& a, bool back, hipStream_t s)
+{
+    constexpr int per = threads_of(TPR) / TPR;
+    const dim3 block(threads_of(TPR));
+    if (!back) {
+        hipLaunchKernelGGL((norm_rows<E, W, TPR, CH>), grid_of(((int64_t)a.rows + per - 1) / per), block, 0, s, a);
+        return hipGetLastError();
+    }
+    const int groups = norm_partials(a.rows, a.width);
+    const auto kernel = a.y ? (a.dw ? norm_grad<E, W, TPR, CH, true, true> : norm_grad<E, W, TPR, CH, true, false>)
+                            : norm_grad<E, W, TPR, CH, false, true>;
+    hipLaunchKernelGGL(kernel, dim3((groups + per - 1) / per), block, 0, s, a, groups);
+    return hipGetLastError();
+}
+
+template <class E, class W>
+hipError_t launch_wide(const NormArgs& a, bool back, hipStream_t s)
+{
+    if (!back) {
+        hipLaunchKernelGGL((norm_rows_wide<E, W>), grid_of(a.rows), dim3(1024), 0, s, a);
+        return hipGetLastError();
+    }
+    if (a.dw) {  // before dx, which may stand on dy
+        const int groups = norm_partials(a.rows, a.width);
+        const unsigned strips = (a.width + kColumnThreads * 8 - 1) / (kColumnThreads * 8);
+        hipLaunchKernelGGL(norm_dw_wide<E>, grid_of((int64_t)groups * strips), dim3(kColumnThreads), 0, s, a, groups,
+                           strips);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    if (a.y)
+        hipLaunchKernelGGL((norm_dx_wide<E, W>), grid_of(a.rows), dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class E, class W>
+hipError_t launch_width(const NormArgs& a, bool back, hipStream_t s)
+{
+    if (a.width <= 512)
+        return launch_rows<E, W, 64, 1>(a, back, s);
+    if (a.width <= 1024)
+        return launch_rows<E, W, 64, 2>(a, back, s);
+    if (a.width <= 2048)
+        return launch_rows<E, W, 256, 1>(a, back, s);
+    if (a.width <= 4096)
+        return launch_rows<E, W, 256, 2>(a, back, s);
+    if (a.width <= 8192)
+        return launch_rows<E, W, 512, 2>(a, back, s);
+    if (a.width <= kMaxResident)
+        return launch_rows<E, W, 1024, 2>(a, back, s);
+    return launch_wide<E, W>(a, back, s);
+}
+
+template <class E>
+hipError_t launch_weight(const NormArgs& a, bool back, hipStream_t s)
+{
+    return a.w_dtype == a.dtype ? launch_width<E, E>(a, back, s) : launch_width<E, F32>(a, back, s);
+}
+
+hipError_t launch_type(const NormArgs& a, bool back, hipStream_t s)
+{
+    switch (a.dtype) {
+    case MOE_DTYPE_BF16: return launch_weight<Bf16>(a, back, s);
+    case MOE_DTYPE_F16: return launch_weight<F16>(a, back, s);
+    case MOE_DTYPE_F32: return launch_width<F32, F32>(a, back, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) { return launch_type(a, false, s); }
+
+hipError_t launch_rms_norm_bwd(const NormArgs& a, hipStream_t s)
+{
+    if (a.rows > 0) {
+        const hipError_t e = launch_type(a, true, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (a.dw)
+        hipLaunchKernelGGL(norm_dw_sum, dim3((a.width + 63) / 64), dim3(256), 0, s, a.partial,
+                           norm_partials(a.rows, a.width), a.width, a.dw);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -129,6 +129,70 @@ moe::MxQuantArgs mx_args(int32_t rows, int32_t cols, int32_t dtype, const void* 
     return a;
 }
 
+// Bytes per row and alignment of the scales of 8-bit rows; false for an unknown format.
+bool sf_layout(int32_t format, int64_t cols, int64_t& row_bytes, int& align)
+{
+    row_bytes = format == MOE_SF_F32_128 ? cols / 128 * 4 : cols / 32;
+    align = format == MOE_SF_F32_128 ? 4 : 1;
+    return format == MOE_SF_F32_128 || format == MOE_SF_UE8M0_32;
+}
+
+int sf_block(int32_t format) { return format == MOE_SF_F32_128 ? 128 : 32; }
+
+// Whether two row matrices are one and the same.
+bool same_rows(const void* a, int64_t a_ld, const void* b, int64_t b_ld) { return a == b && a_ld == b_ld; }
+
+// Whether an output of a call overlaps an input or another output; bit i of
+// allowed[o]: output o may stand on input i.
+template <int O, int I>
+bool any_overlap(const Span (&out)[O], const Span (&in)[I], const unsigned (&allowed)[O])
+{
+    for (int o = 0; o < O; ++o) {
+        for (int i = 0; i < I; ++i)
+            if (!(allowed[o] >> i & 1) && overlap(out[o], in[i]))
+                return true;
+        for (int p = 0; p < o; ++p)
+            if (overlap(out[o], out[p]))
+                return true;
+    }
+    return false;
+}
+
+int check_gate(int32_t T, int32_t E, int32_t K, int32_t dtype, int32_t score)
+{
+    if (T < 0 || E < 1 || K < 1 || K > E || elem_bytes(dtype) < 2 ||
+        (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID))
+        return MOE_ERR_INVALID_ARG;
+    if (E > 1024 || K > 64 || T >= (1 << 28))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+int check_norm(int32_t rows, int32_t width, int32_t dtype, int32_t w_dtype)
+{
+    if (rows < 0 || width < 1 || elem_bytes(dtype) < 2 || (w_dtype != dtype && w_dtype != MOE_DTYPE_F32))
+        return MOE_ERR_INVALID_ARG;
+    if (rows >= (1 << 28) || width >= (1 << 24))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+size_t norm_workspace(int32_t rows, int32_t width)
+{
+    return static_cast<size_t>(moe::norm_partials(rows, width)) * width * 4;
+}
+
+int check_swiglu(int32_t R, int32_t inner, int32_t dtype, bool codes, int32_t format)
+{
+    int64_t unused;
+    int align;
+    if (R < 0 || inner < 1 || elem_bytes(dtype) < 2 || (codes && !sf_layout(format, inner, unused, align)))
+        return MOE_ERR_INVALID_ARG;
+    if (R >= (1 << 28) || inner >= (1 << 23) || (codes && inner % sf_block(format) != 0))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
 int check_gemm(int32_t groups, int32_t rows, int32_t n, int32_t k)
 {
     if (groups < 1 || rows < 0 || n < 0 || k < 1)
@@ -314,6 +378,287 @@ int moe_gemm_mxfp4_info(int32_t groups, int32_t rows, int32_t n, int32_t k, int3
     if (rc == MOE_OK)
         moe::gemm_mxfp4_tile(groups == 0 ? 1 : groups, rows, n, k, groups != 0, *tile_m, *tile_n);
     return rc;
+}
+
+int moe_gate(int32_t T, int32_t E, int32_t K, int32_t dtype, const void* logits, int64_t logits_ld,
+             const float* bias, const uint8_t* mask, int32_t score, int32_t groups,
+             int32_t top_groups, int32_t group_top, int32_t renorm, float scale,
+             int32_t* topk_idx, float* topk_w, void* stream)
+{
+    int rc = check_gate(T, E, K, dtype, score);
+    if (rc != MOE_OK)
+        return rc;
+    if (groups < 1 || E % groups != 0 || top_groups < 1 || top_groups > groups || group_top < 1 ||
+        group_top > E / groups || K > E / groups * top_groups || (groups == 1 && group_top != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (groups > 64)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0)
+        return MOE_OK;
+    const int es = elem_bytes(dtype);
+    const int64_t ld = stride(logits_ld, E), slots = static_cast<int64_t>(T) * K;
+    if (!logits || !topk_idx || !topk_w || ld < 0 || misaligned(logits, es) || misaligned(bias, 4) ||
+        misaligned(topk_idx, 4) || misaligned(topk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    const Span out[2] = {span(topk_idx, 1, slots, slots, 4), span(topk_w, 1, slots, slots, 4)};
+    const Span in[3] = {span(logits, T, ld, E, es), span(bias, 1, E, E, 4), span(mask, 1, T, T, 1)};
+    const unsigned allowed[2] = {};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::GateArgs a{};
+    a.T = T; a.E = E; a.K = K; a.dtype = dtype;
+    a.logits = static_cast<const char*>(logits);
+    a.ld = ld * es;
+    a.bias = bias;
+    a.mask = mask;
+    a.score = score;
+    a.groups = groups; a.top_groups = top_groups; a.group_top = group_top;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    return launched(moe::launch_gate(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_gate_bwd(int32_t T, int32_t E, int32_t K, int32_t dtype, const void* logits,
+                 int64_t logits_ld, const int32_t* topk_idx, const float* dw, int32_t score,
+                 int32_t renorm, float scale, void* dlogits, int64_t dlogits_ld, void* stream)
+{
+    int rc = check_gate(T, E, K, dtype, score);
+    if (rc != MOE_OK)
+        return rc;
+    if (T == 0)
+        return MOE_OK;
+    const int es = elem_bytes(dtype);
+    const int64_t ld = stride(logits_ld, E), old = stride(dlogits_ld, E), slots = static_cast<int64_t>(T) * K;
+    if (!logits || !topk_idx || !dw || !dlogits || ld < 0 || old < 0 || misaligned(logits, es) ||
+        misaligned(dlogits, es) || misaligned(topk_idx, 4) || misaligned(dw, 4))
+        return MOE_ERR_INVALID_ARG;
+    const Span out[1] = {span(dlogits, T, old, E, es)};
+    const Span in[3] = {span(logits, T, ld, E, es), span(topk_idx, 1, slots, slots, 4),
+                        span(dw, 1, slots, slots, 4)};
+    const unsigned allowed[1] = {};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::GateArgs a{};
+    a.T = T; a.E = E; a.K = K; a.dtype = dtype;
+    a.logits = static_cast<const char*>(logits);
+    a.ld = ld * es;
+    a.score = score;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.idx = const_cast<int32_t*>(topk_idx);
+    a.w = const_cast<float*>(dw);
+    a.dlogits = static_cast<char*>(dlogits);
+    a.dlogits_ld = old * es;
+    return launched(moe::launch_gate_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_rms_norm(int32_t rows, int32_t width, int32_t dtype, const void* x, int64_t x_ld,
+                 const void* residual, int64_t residual_ld, const void* weight, int32_t w_dtype,
+                 float eps, void* z, int64_t z_ld, float* rstd, void* y, int64_t y_ld,
+                 uint8_t* codes, void* sf, int32_t sf_format, void* stream)
+{
+    int rc = check_norm(rows, width, dtype, w_dtype);
+    if (rc != MOE_OK)
+        return rc;
+    int64_t sf_row = 0;
+    int sf_align = 1;
+    if (codes || sf) {
+        if (!sf_layout(sf_format, width, sf_row, sf_align))
+            return MOE_ERR_INVALID_ARG;
+        if (width % sf_block(sf_format) != 0)
+            return MOE_ERR_UNSUPPORTED_SHAPE;
+    }
+    if (rows == 0)
+        return MOE_OK;
+    const int es = elem_bytes(dtype), ws = elem_bytes(w_dtype);
+    const int64_t xld = stride(x_ld, width), rld = residual ? stride(residual_ld, width) : 0,
+                  zld = z ? stride(z_ld, width) : 0, yld = y ? stride(y_ld, width) : 0;
+    if (!x || (!y && !codes) || !codes != !sf || (z && !residual) || xld < 0 || rld < 0 || zld < 0 ||
+        yld < 0 || misaligned(x, es) || misaligned(residual, es) || misaligned(z, es) ||
+        misaligned(y, es) || misaligned(weight, ws) || misaligned(rstd, 4) || misaligned(codes, 8) ||
+        misaligned(sf, sf_align))
+        return MOE_ERR_INVALID_ARG;
+    const Span out[5] = {span(z, rows, zld, width, es), span(y, rows, yld, width, es),
+                         span(rstd, 1, rows, rows, 4), span(codes, rows, width, width, 1),
+                         span(sf, rows, sf_row, sf_row, 1)};
+    const Span in[3] = {span(x, rows, xld, width, es), span(residual, rows, rld, width, es),
+                        span(weight, 1, width, width, ws)};
+    const auto onto = [&](const void* p, int64_t ld) {
+        return p ? (same_rows(p, ld, x, xld) ? 1u : 0u) | (residual && same_rows(p, ld, residual, rld) ? 2u : 0u) : 0u;
+    };
+    const unsigned allowed[5] = {onto(z, zld), onto(y, yld)};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::NormArgs a{};
+    a.rows = rows; a.width = width; a.dtype = dtype; a.w_dtype = w_dtype;
+    a.x = static_cast<const char*>(x); a.x_ld = xld * es;
+    a.res = static_cast<const char*>(residual); a.res_ld = rld * es;
+    a.weight = static_cast<const char*>(weight);
+    a.eps = eps;
+    a.z = static_cast<char*>(z); a.z_ld = zld * es;
+    a.rstd = rstd;
+    a.y = static_cast<char*>(y); a.y_ld = yld * es;
+    a.codes = codes; a.sf = sf; a.sf_format = sf_format;
+    return launched(moe::launch_rms_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_rms_norm_bwd(int32_t rows, int32_t width, int32_t dtype, const void* dy, int64_t dy_ld,
+                     const void* z, int64_t z_ld, const void* weight, int32_t w_dtype,
+                     const float* rstd, const void* dz, int64_t dz_ld, void* dx, int64_t dx_ld,
+                     float* dw, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = check_norm(rows, width, dtype, w_dtype);
+    if (rc != MOE_OK)
+        return rc;
+    if (!dx && !dw)
+        return rows == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
+    if (rows == 0 && !dw)
+        return MOE_OK;
+    const int es = elem_bytes(dtype), ws = elem_bytes(w_dtype);
+    const int64_t dyld = stride(dy_ld, width), zld = stride(z_ld, width),
+                  dzld = dz ? stride(dz_ld, width) : 0, dxld = dx ? stride(dx_ld, width) : 0;
+    if ((rows > 0 && (!dy || !z || !rstd)) || dyld < 0 || zld < 0 || dzld < 0 || dxld < 0 ||
+        misaligned(dy, es) || misaligned(z, es) || misaligned(dz, es) || misaligned(dx, es) ||
+        misaligned(weight, ws) || misaligned(rstd, 4) || misaligned(dw, 4) || misaligned(workspace, 16))
+        return MOE_ERR_INVALID_ARG;
+    const size_t need = dw ? norm_workspace(rows, width) : 0;
+    if (need > 0 && !workspace)
+        return MOE_ERR_INVALID_ARG;
+    if (need > workspace_bytes)
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const Span out[3] = {span(dx, rows, dxld, width, es), span(dw, 1, width, width, 4),
+                         span(need ? workspace : nullptr, 1, need, need, 1)};
+    const Span in[5] = {span(dy, rows, dyld, width, es), span(dz, rows, dzld, width, es),
+                        span(z, rows, zld, width, es), span(weight, 1, width, width, ws),
+                        span(rstd, 1, rows, rows, 4)};
+    const unsigned allowed[3] = {!dx ? 0u : (same_rows(dx, dxld, dy, dyld) ? 1u : 0u) |
+                                                (dz && same_rows(dx, dxld, dz, dzld) ? 2u : 0u)};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::NormArgs a{};
+    a.rows = rows; a.width = width; a.dtype = dtype; a.w_dtype = w_dtype;
+    a.x = static_cast<const char*>(dy); a.x_ld = dyld * es;
+    a.res = static_cast<const char*>(dz); a.res_ld = dzld * es;
+    a.weight = static_cast<const char*>(weight);
+    a.z = static_cast<char*>(const_cast<void*>(z)); a.z_ld = zld * es;
+    a.rstd = const_cast<float*>(rstd);
+    a.y = static_cast<char*>(dx); a.y_ld = dxld * es;
+    a.dw = dw;
+    a.partial = static_cast<float*>(workspace);
+    return launched(moe::launch_rms_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_rms_norm_bwd_workspace_bytes(int32_t rows, int32_t width, size_t* bytes)
+{
+    if (!bytes)
+        return MOE_ERR_INVALID_ARG;
+    const int rc = check_norm(rows, width, MOE_DTYPE_F32, MOE_DTYPE_F32);
+    if (rc == MOE_OK)
+        *bytes = norm_workspace(rows, width);
+    return rc;
+}
+
+int moe_swiglu(int32_t R, int32_t inner, int32_t dtype, const void* gu, int64_t gu_ld, float clamp,
+               const int32_t* row_src, const int32_t* used, void* h, int64_t h_ld,
+               uint8_t* h_codes, void* h_sf, uint8_t* gu_codes, void* gu_sf, int32_t sf_format,
+               void* stream)
+{
+    const bool eight = h_codes || h_sf || gu_codes || gu_sf;
+    int rc = check_swiglu(R, inner, dtype, eight, sf_format);
+    if (rc != MOE_OK)
+        return rc;
+    if (R == 0)
+        return MOE_OK;
+    const int es = elem_bytes(dtype);
+    const int64_t width = 2 * static_cast<int64_t>(inner), gld = stride(gu_ld, width),
+                  hld = h ? stride(h_ld, inner) : 0;
+    int64_t sf_row = 0;
+    int sf_align = 1;
+    if (eight)
+        sf_layout(sf_format, inner, sf_row, sf_align);
+    if (!gu || (!h && !h_codes && !gu_codes) || !h_codes != !h_sf || !gu_codes != !gu_sf || gld < 0 ||
+        hld < 0 || misaligned(gu, es) || misaligned(h, es) || misaligned(h_codes, 8) ||
+        misaligned(gu_codes, 8) || misaligned(h_sf, sf_align) || misaligned(gu_sf, sf_align) ||
+        misaligned(row_src, 4) || misaligned(used, 4))
+        return MOE_ERR_INVALID_ARG;
+    const Span out[5] = {span(h, R, hld, inner, es), span(h_codes, R, inner, inner, 1),
+                         span(h_sf, R, sf_row, sf_row, 1), span(gu_codes, R, width, width, 1),
+                         span(gu_sf, R, 2 * sf_row, 2 * sf_row, 1)};
+    const Span in[3] = {span(gu, R, gld, width, es), span(row_src, 1, R, R, 4), span(used, 1, 1, 1, 4)};
+    const unsigned allowed[5] = {};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::SwigluArgs a{};
+    a.R = R; a.inner = inner; a.dtype = dtype;
+    a.gu = static_cast<const char*>(gu); a.gu_ld = gld * es;
+    a.clamp = clamp;
+    a.row_src = row_src; a.used = used;
+    a.h = static_cast<char*>(h); a.h_ld = hld * es;
+    a.h_codes = h_codes; a.h_sf = h_sf;
+    a.gu_codes = gu_codes; a.gu_sf = gu_sf;
+    a.sf_format = sf_format;
+    return launched(moe::launch_swiglu(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_swiglu_bwd(int32_t R, int32_t inner, int32_t dtype, const void* dh, int64_t dh_ld,
+                   const void* gu, int64_t gu_ld, const uint8_t* gu_codes, const void* gu_sf,
+                   int32_t sf_format, float clamp, const int32_t* row_src, const int32_t* used,
+                   void* dgu, int64_t dgu_ld, void* stream)
+{
+    const bool eight = gu_codes || gu_sf;
+    int rc = check_swiglu(R, inner, dtype, eight, sf_format);
+    if (rc != MOE_OK)
+        return rc;
+    if (R == 0)
+        return MOE_OK;
+    const int es = elem_bytes(dtype);
+    const int64_t width = 2 * static_cast<int64_t>(inner), hld = stride(dh_ld, inner),
+                  gld = gu ? stride(gu_ld, width) : 0, old = stride(dgu_ld, width);
+    int64_t sf_row = 0;
+    int sf_align = 1;
+    if (eight)
+        sf_layout(sf_format, width, sf_row, sf_align);
+    if (!dh || !dgu || !gu == !gu_codes || !gu_codes != !gu_sf || hld < 0 || gld < 0 || old < 0 ||
+        misaligned(dh, es) || misaligned(gu, es) || misaligned(dgu, es) || misaligned(gu_codes, 8) ||
+        misaligned(gu_sf, sf_align) || misaligned(row_src, 4) || misaligned(used, 4))
+        return MOE_ERR_INVALID_ARG;
+    const Span out[1] = {span(dgu, R, old, width, es)};
+    const Span in[6] = {span(gu, R, gld, width, es), span(dh, R, hld, inner, es),
+                        span(gu_codes, R, width, width, 1), span(gu_sf, R, sf_row, sf_row, 1),
+                        span(row_src, 1, R, R, 4), span(used, 1, 1, 1, 4)};
+    const unsigned allowed[1] = {gu && same_rows(dgu, old, gu, gld) ? 1u : 0u};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::SwigluArgs a{};
+    a.R = R; a.inner = inner; a.dtype = dtype;
+    a.gu = static_cast<const char*>(gu); a.gu_ld = gld * es;
+    a.clamp = clamp;
+    a.row_src = row_src; a.used = used;
+    a.h = static_cast<char*>(const_cast<void*>(dh)); a.h_ld = hld * es;
+    a.gu_codes = const_cast<uint8_t*>(gu_codes); a.gu_sf = const_cast<void*>(gu_sf);
+    a.sf_format = sf_format;
+    a.dgu = static_cast<char*>(dgu); a.dgu_ld = old * es;
+    return launched(moe::launch_swiglu_bwd(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

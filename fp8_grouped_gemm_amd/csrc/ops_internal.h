@@ -46,6 +46,68 @@ struct MxGemmArgs {
     int64_t y_ld;              // bytes
 };
 
+struct GateArgs {
+    int32_t T, E, K, dtype;
+    const char* logits;
+    int64_t ld;                // bytes
+    const float* bias;         // may be null
+    const uint8_t* mask;       // may be null
+    int32_t score;             // MOE_SCORE_*
+    int32_t groups, top_groups, group_top;
+    bool renorm;
+    float scale;
+    int32_t* idx;              // written by the choice, read by its gradient
+    float* w;                  // topk_w; the gradient: dw, read
+    char* dlogits;
+    int64_t dlogits_ld;        // bytes
+};
+
+struct NormArgs {
+    int32_t rows, width, dtype, w_dtype;
+    const char* x;             // backward: dy
+    int64_t x_ld;              // bytes, as all strides here
+    const char* res;           // may be null; backward: dz
+    int64_t res_ld;
+    const char* weight;        // may be null
+    float eps;
+    char* z;                   // may be null; backward: read
+    int64_t z_ld;
+    float* rstd;               // may be null; backward: read
+    char* y;                   // may be null; backward: dx
+    int64_t y_ld;
+    uint8_t* codes;            // may be null
+    void* sf;
+    int32_t sf_format;         // MOE_SF_*
+    float* dw;                 // backward, may be null
+    float* partial;            // [norm_partials(...), width]
+};
+
+struct SwigluArgs {
+    int32_t R, inner, dtype;
+    const char* gu;            // null in a backward pass from codes
+    int64_t gu_ld;             // bytes, as all strides here
+    float clamp;
+    const int32_t* row_src;    // may be null
+    const int32_t* used;       // may be null: R
+    char* h;                   // may be null; backward: dh, read
+    int64_t h_ld;
+    uint8_t* h_codes;          // may be null
+    void* h_sf;
+    uint8_t* gu_codes;         // may be null; backward: read
+    void* gu_sf;
+    int32_t sf_format;         // MOE_SF_*
+    char* dgu;                 // backward
+    int64_t dgu_ld;
+};
+
+hipError_t launch_gate(const GateArgs& a, hipStream_t s);
+hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t s);
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_rms_norm_bwd(const NormArgs& a, hipStream_t s);
+// Rows of partial sums of dw that a backward call writes (host only).
+int norm_partials(int rows, int width);
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
+hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t s);
 hipError_t launch_permute(const RowsArgs& a, hipStream_t s);
 hipError_t launch_unpermute(const RowsArgs& a, hipStream_t s);  // also permute's gradient
 hipError_t launch_unpermute_bwd(const RowsArgs& a, hipStream_t s);

@@ -1,6 +1,8 @@
 """Row operators of libmoe_fp8.so (include/moe_ops.h): token rows into expert
-order and back with their gradients, microscaled 4-bit quantisation, and the
-product of two microscaled 4-bit matrices.
+order and back with their gradients, microscaled 4-bit quantisation, the
+product of two microscaled 4-bit matrices, and around the experts' products the
+router's choice, the residual norm and SwiGLU with 8-bit rows, each with its
+gradient.
 
 One function per entry point.  Tensors are checked here (type, shape, layout,
 device), before the library's own checks; outputs are allocated where none
@@ -22,10 +24,16 @@ MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
 MOE_DTYPE_F32 = 2
 MOE_DTYPE_U8 = 3
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_SF_F32_128 = 0
+MOE_SF_UE8M0_32 = 1
 
 EXPORTED_SYMBOLS = (
     "moe_permute", "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd",
     "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4", "moe_gemm_mxfp4_info",
+    "moe_gate", "moe_gate_bwd", "moe_rms_norm", "moe_rms_norm_bwd",
+    "moe_rms_norm_bwd_workspace_bytes", "moe_swiglu", "moe_swiglu_bwd",
 )
 
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
@@ -41,6 +49,7 @@ def ops_lib():
     if _ops is None:
         L = lib()
         vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        f32, size = ctypes.c_float, ctypes.c_size_t
         L.moe_permute.argtypes = [i32] * 5 + [vp, i64, vp, vp, vp, vp, i64, vp]
         L.moe_permute_bwd.argtypes = [i32] * 5 + [vp, i64, vp, vp, i64, vp]
         L.moe_unpermute.argtypes = [i32] * 5 + [vp, i64, vp, vp, vp, i64, vp]
@@ -50,6 +59,15 @@ def ops_lib():
         L.moe_dequantize_mxfp4.argtypes = [i32] * 3 + [vp, vp, vp, i64, vp]
         L.moe_gemm_mxfp4.argtypes = [i32] * 5 + [vp] * 6 + [i32, vp, i64, vp]
         L.moe_gemm_mxfp4_info.argtypes = [i32] * 4 + [vp] * 2
+        L.moe_gate.argtypes = [i32] * 4 + [vp, i64, vp, vp] + [i32] * 5 + [f32, vp, vp, vp]
+        L.moe_gate_bwd.argtypes = [i32] * 4 + [vp, i64, vp, vp, i32, i32, f32, vp, i64, vp]
+        L.moe_rms_norm.argtypes = ([i32] * 3 + [vp, i64, vp, i64, vp, i32, f32, vp, i64, vp, vp, i64,
+                                                vp, vp, i32, vp])
+        L.moe_rms_norm_bwd.argtypes = ([i32] * 3 + [vp, i64, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp,
+                                                    vp, size, vp])
+        L.moe_rms_norm_bwd_workspace_bytes.argtypes = [i32, i32, vp]
+        L.moe_swiglu.argtypes = [i32] * 3 + [vp, i64, f32, vp, vp, vp, i64] + [vp] * 4 + [i32, vp]
+        L.moe_swiglu_bwd.argtypes = [i32] * 3 + [vp, i64, vp, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]
         for name in EXPORTED_SYMBOLS:
             getattr(L, name).restype = ctypes.c_int
         _ops = L
@@ -173,6 +191,46 @@ def _used(offsets, dev):
     if n < 1:
         raise ValueError("offsets: empty")
     return _dense(offsets, "offsets", dev, torch.int32, n) + 4 * (n - 1)
+
+
+_SF_BLOCK = {MOE_SF_F32_128: (128, torch.float32), MOE_SF_UE8M0_32: (32, torch.uint8)}
+
+
+def _new_codes(rows, cols, sf_format, codes, sf, device):
+    """The given (or new) code and scale tensors of 8-bit rows in a format."""
+    if sf_format not in _SF_BLOCK:
+        raise ValueError(f"sf_format {sf_format}")
+    block, dtype = _SF_BLOCK[sf_format]
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.uint8, device=device)
+    if sf is None:
+        sf = torch.empty(rows, cols // block, dtype=dtype, device=device)
+    return codes, sf
+
+
+def _codes_at(codes, sf, name, dev, rows, cols, sf_format):
+    """Checks 8-bit rows of a format; returns their addresses."""
+    block, dtype = _SF_BLOCK[sf_format]
+    return (_dense(codes, name + "codes", dev, torch.uint8, (rows, cols)),
+            _dense(sf, name + "sf", dev, dtype, (rows, cols // block)))
+
+
+def _sf_format(sf, name):
+    """The format that a scale tensor's type tells."""
+    for fmt, (_, dtype) in _SF_BLOCK.items():
+        if sf.dtype is dtype:
+            return fmt
+    raise ValueError(f"{name}: {sf.dtype}, expected float32 (per 128 columns) or uint8 (UE8M0, per 32)")
+
+
+def _norm_weight(weight, dev, dtype, width):
+    """Checks a norm's weight (its rows' type or f32; None: 1); returns address and dtype code."""
+    if weight is None:
+        return None, MOE_DTYPE_F32
+    if weight.requires_grad and torch.is_grad_enabled():
+        _lost("weight")
+    t = torch.float32 if weight.dtype is torch.float32 else dtype
+    return _dense(weight, "weight", dev, t, (width,)), _DTYPES[t]
 
 
 def moe_permute(x, row_src, src_row, offsets, out=None, stream=None):
@@ -381,3 +439,229 @@ def moe_gemm_mxfp4_info(rows, n, k, groups=0):
     _check(ops_lib().moe_gemm_mxfp4_info(groups, rows, n, k, ctypes.addressof(m),
                                          ctypes.addressof(w)), "moe_gemm_mxfp4_info")
     return {"tile_m": m.value, "tile_n": w.value}
+
+
+def moe_gate(logits, top_k, bias=None, mask=None, score=MOE_SCORE_SOFTMAX, groups=1, top_groups=1,
+             group_top=1, renorm=True, scale=1.0, topk_idx=None, topk_w=None, stream=None):
+    """The router's choice: (topk_idx int32 [T, K], topk_w f32 [T, K]) of logits
+    [T, E], largest first, ties to the lower id, -1 and 0 where no expert is left.
+    Scores are the logits' softmax or sigmoid; bias f32 [E] shifts them for the choice
+    alone; groups > 1: the top_groups groups with the largest sums of their group_top
+    best experts are chosen from; renorm: weights divided by their sum; scale: times
+    that.  mask bool or uint8 [T]: tokens with 0 get no expert."""
+    if not _here(logits, stream):
+        return _elsewhere(moe_gate, logits, stream, logits, top_k, bias, mask, score, groups, top_groups,
+                          group_top, renorm, scale, topk_idx, topk_w)
+    dev = logits.get_device()
+    dt, T, E = _matrix(logits, "logits", _DTYPES)
+    _int32("sizes", max(map(abs, (top_k, score, groups, top_groups, group_top))))
+    slots = (T, max(top_k, 0))
+    _int32("topk_idx", slots[0] * slots[1])
+    if mask is not None and mask.dtype is torch.bool:
+        mask = mask.view(torch.uint8)
+    given = tuple(t for t in (topk_idx, topk_w) if t is not None)
+    if topk_idx is None:
+        topk_idx = torch.empty(slots, dtype=torch.int32, device=logits.device)
+    if topk_w is None:
+        topk_w = torch.empty(slots, dtype=torch.float32, device=logits.device)
+    elif topk_w.requires_grad and torch.is_grad_enabled():
+        _lost("topk_w")
+    _check(ops_lib().moe_gate(
+        T, E, top_k, dt, logits.data_ptr(), _rows(logits, "logits", dev, logits.dtype, T, E),
+        None if bias is None else _dense(bias, "bias", dev, torch.float32, (E,)),
+        None if mask is None else _dense(mask, "mask", dev, torch.uint8, (T,)),
+        score, groups, top_groups, group_top, bool(renorm), scale,
+        _dense(topk_idx, "topk_idx", dev, torch.int32, slots),
+        _dense(topk_w, "topk_w", dev, torch.float32, slots), _raw_stream(dev)), "moe_gate")
+    if given:
+        _wrote(given)
+    return topk_idx, topk_w
+
+
+def moe_gate_bwd(logits, topk_idx, dw, score=MOE_SCORE_SOFTMAX, renorm=True, scale=1.0, out=None, stream=None):
+    """Gradient of moe_gate's weights: dlogits [T, E] for dw f32 [T, K], the choice
+    topk_idx int32 [T, K] fixed."""
+    if not _here(logits, stream):
+        return _elsewhere(moe_gate_bwd, logits, stream, logits, topk_idx, dw, score, renorm, scale, out)
+    dev = logits.get_device()
+    dt, T, E = _matrix(logits, "logits", _DTYPES)
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [T, K]")
+    K = topk_idx.shape[1]
+    _int32("topk_idx", max(T * K, abs(score)))
+    if dw.requires_grad and torch.is_grad_enabled():
+        _lost("dw")
+    given = out
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    _check(ops_lib().moe_gate_bwd(
+        T, E, K, dt, logits.data_ptr(), _rows(logits, "logits", dev, logits.dtype, T, E),
+        _dense(topk_idx, "topk_idx", dev, torch.int32, (T, K)), _dense(dw, "dw", dev, torch.float32, (T, K)),
+        score, bool(renorm), scale, out.data_ptr(), _rows(out, "out", dev, logits.dtype, T, E),
+        _raw_stream(dev)), "moe_gate_bwd")
+    if given is not None:
+        _wrote((given,))
+    return out
+
+
+def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, need_y=True, sf_format=None, z=None, rstd=None, y=None,
+                 codes=None, sf=None, stream=None):
+    """Residual and root-mean-square norm of rows x [T, W]: (z, rstd, y, codes, sf).
+    z = x + residual (None without a residual; z=residual or z=x: in place), rstd f32
+    [T], y = z * rstd * weight in x's type (need_y), and y in 8 bits in a format
+    (sf_format MOE_SF_F32_128: f32 scales per 128 columns, MOE_SF_UE8M0_32: UE8M0 codes
+    per 32; None: codes and sf None).  weight [W] in x's type or f32 (None: 1)."""
+    if not _here(x, stream):
+        return _elsewhere(moe_rms_norm, x, stream, x, weight, residual, eps, need_y, sf_format, z, rstd, y, codes,
+                          sf)
+    dev = x.get_device()
+    dt, T, W = _matrix(x, "x", _DTYPES)
+    given = tuple(t for t, need in ((z, True), (rstd, True), (y, need_y), (codes, sf_format is not None),
+                                    (sf, sf_format is not None)) if need and t is not None)
+    res_at = z_at = y_at = codes_at = sf_at = None
+    res_ld = z_ld = y_ld = 0
+    if residual is not None:
+        res_at, res_ld = residual.data_ptr(), _rows(residual, "residual", dev, x.dtype, T, W)
+        if z is None:
+            z = torch.empty(T, W, dtype=x.dtype, device=x.device)
+        z_at, z_ld = z.data_ptr(), _rows(z, "z", dev, x.dtype, T, W)
+    elif z is not None:
+        raise ValueError("z: without a residual it is x")
+    if rstd is None:
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    if need_y:
+        if y is None:
+            y = torch.empty(T, W, dtype=x.dtype, device=x.device)
+        y_at, y_ld = y.data_ptr(), _rows(y, "y", dev, x.dtype, T, W)
+    if sf_format is not None:
+        codes, sf = _new_codes(T, W, sf_format, codes, sf, x.device)
+        codes_at, sf_at = _codes_at(codes, sf, "", dev, T, W, sf_format)
+    w_at, w_dt = _norm_weight(weight, dev, x.dtype, W)
+    _check(ops_lib().moe_rms_norm(
+        T, W, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, T, W), res_at, res_ld, w_at, w_dt, eps, z_at, z_ld,
+        _dense(rstd, "rstd", dev, torch.float32, (T,)), y_at, y_ld, codes_at, sf_at, sf_format or 0,
+        _raw_stream(dev)), "moe_rms_norm")
+    if given:
+        _wrote(given)
+    eight = sf_format is not None
+    return z, rstd, (y if need_y else None), (codes if eight else None), (sf if eight else None)
+
+
+def moe_rms_norm_bwd_workspace_bytes(rows, width):
+    """Bytes of workspace that moe_rms_norm_bwd needs for the weight's gradient."""
+    _int32("sizes", max(map(abs, (rows, width))))
+    n = ctypes.c_size_t()
+    _check(ops_lib().moe_rms_norm_bwd_workspace_bytes(rows, width, ctypes.addressof(n)),
+           "moe_rms_norm_bwd_workspace_bytes")
+    return n.value
+
+
+def moe_rms_norm_bwd(dy, z, rstd, weight=None, dz=None, dx=None, dw=None, need_dx=True, need_dw=True,
+                     workspace=None, stream=None):
+    """Gradients of moe_rms_norm for dy [T, W], through the z (without a residual: x) and
+    rstd it returned: (dx [T, W], dw f32 [W]); dx is that of x and of the residual
+    alike, dz [T, W] the gradient that reaches z on its other way (None: 0).  need_dx /
+    need_dw False: that one is None.  workspace uint8, at least
+    moe_rms_norm_bwd_workspace_bytes (None: allocated)."""
+    if not _here(dy, stream):
+        return _elsewhere(moe_rms_norm_bwd, dy, stream, dy, z, rstd, weight, dz, dx, dw, need_dx, need_dw,
+                          workspace)
+    dev = dy.get_device()
+    if not (need_dx or need_dw):
+        _check(MOE_ERR_INVALID_ARG, "moe_rms_norm_bwd")
+    dt, T, W = _matrix(dy, "dy", _DTYPES)
+    given = tuple(t for t, need in ((dx, need_dx), (dw, need_dw)) if need and t is not None)
+    dz_at = dx_at = dw_at = ws_at = None
+    dz_ld = dx_ld = ws_bytes = 0
+    if dz is not None:
+        dz_at, dz_ld = dz.data_ptr(), _rows(dz, "dz", dev, dy.dtype, T, W)
+    if need_dx:
+        if dx is None:
+            dx = torch.empty(T, W, dtype=dy.dtype, device=dy.device)
+        dx_at, dx_ld = dx.data_ptr(), _rows(dx, "dx", dev, dy.dtype, T, W)
+    if need_dw:
+        if dw is None:
+            dw = torch.empty(W, dtype=torch.float32, device=dy.device)
+        elif dw.requires_grad and torch.is_grad_enabled():
+            _lost("dw")
+        dw_at = _dense(dw, "dw", dev, torch.float32, (W,))
+        if workspace is None:
+            workspace = torch.empty(moe_rms_norm_bwd_workspace_bytes(T, W), dtype=torch.uint8, device=dy.device)
+        ws_bytes = workspace.numel()
+        ws_at = _dense(workspace, "workspace", dev, torch.uint8, ws_bytes)
+    w_at, w_dt = _norm_weight(weight, dev, dy.dtype, W)
+    _check(ops_lib().moe_rms_norm_bwd(
+        T, W, dt, dy.data_ptr(), _rows(dy, "dy", dev, dy.dtype, T, W), z.data_ptr(),
+        _rows(z, "z", dev, dy.dtype, T, W), w_at, w_dt, _dense(rstd, "rstd", dev, torch.float32, (T,)), dz_at, dz_ld,
+        dx_at, dx_ld, dw_at, ws_at, ws_bytes, _raw_stream(dev)), "moe_rms_norm_bwd")
+    if given:
+        _wrote(given)
+    return (dx if need_dx else None), (dw if need_dw else None)
+
+
+def moe_swiglu(gu, row_src=None, offsets=None, clamp=0.0, sf_format=None, need_h=True, need_h8=False,
+               need_gu8=False, h=None, h_codes=None, h_sf=None, gu_codes=None, gu_sf=None, stream=None):
+    """h = silu(gate) * up of pool rows gu [R, 2 I] (gate, then up): (h, h_codes, h_sf,
+    gu_codes, gu_sf), those not needed None.  need_h: h [R, I] in gu's type; need_h8: h
+    in 8 bits in sf_format, the second product's rows; need_gu8: gu in 8 bits, for
+    moe_swiglu_bwd.  Rows with row_src < 0 and from offsets[-1] on (None: no such
+    rows) are left as they were in every output (a new output: unset).  clamp > 0: gate and up
+    are clamped to [-clamp, clamp] first."""
+    if not _here(gu, stream):
+        return _elsewhere(moe_swiglu, gu, stream, gu, row_src, offsets, clamp, sf_format, need_h, need_h8, need_gu8, h,
+                          h_codes, h_sf, gu_codes, gu_sf)
+    dev = gu.get_device()
+    dt, R, W = _matrix(gu, "gu", _DTYPES)
+    if W % 2:
+        raise ValueError(f"gu: {W} columns, expected gate and up")
+    inner = W // 2
+    given = tuple(t for t, need in ((h, need_h), (h_codes, need_h8), (h_sf, need_h8), (gu_codes, need_gu8),
+                                    (gu_sf, need_gu8)) if need and t is not None)
+    h_at, h_ld, at = None, 0, [None] * 4
+    if need_h:
+        if h is None:
+            h = torch.empty(R, inner, dtype=gu.dtype, device=gu.device)
+        h_at, h_ld = h.data_ptr(), _rows(h, "h", dev, gu.dtype, R, inner)
+    if need_h8:
+        h_codes, h_sf = _new_codes(R, inner, sf_format, h_codes, h_sf, gu.device)
+        at[:2] = _codes_at(h_codes, h_sf, "h_", dev, R, inner, sf_format)
+    if need_gu8:
+        gu_codes, gu_sf = _new_codes(R, W, sf_format, gu_codes, gu_sf, gu.device)
+        at[2:] = _codes_at(gu_codes, gu_sf, "gu_", dev, R, W, sf_format)
+    _check(ops_lib().moe_swiglu(
+        R, inner, dt, gu.data_ptr(), _rows(gu, "gu", dev, gu.dtype, R, W), clamp,
+        None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), _used(offsets, dev), h_at, h_ld,
+        *at, sf_format or 0, _raw_stream(dev)), "moe_swiglu")
+    if given:
+        _wrote(given)
+    return (h if need_h else None, *((h_codes, h_sf) if need_h8 else (None, None)),
+            *((gu_codes, gu_sf) if need_gu8 else (None, None)))
+
+
+def moe_swiglu_bwd(dh, gu=None, gu_codes=None, gu_sf=None, row_src=None, offsets=None, clamp=0.0, out=None,
+                   stream=None):
+    """Gradient of moe_swiglu: dgu [R, 2 I] for dh [R, I], at the input gu, or at its
+    8-bit copy gu_codes [R, 2 I], gu_sf (f32 per 128 columns or UE8M0 per 32).  Rows
+    without a slot are left as they were; out=gu: in place."""
+    if not _here(dh, stream):
+        return _elsewhere(moe_swiglu_bwd, dh, stream, dh, gu, gu_codes, gu_sf, row_src, offsets, clamp, out)
+    dev = dh.get_device()
+    dt, R, inner = _matrix(dh, "dh", _DTYPES)
+    _int32("dh", 2 * inner)
+    if (gu is None) == (gu_codes is None) or (gu_codes is None) != (gu_sf is None):
+        raise ValueError("gu, or gu_codes and gu_sf: exactly one of the two")
+    given, fmt, gu_at, gu_ld, at = out, 0, None, 0, (None, None)
+    if gu is not None:
+        gu_at, gu_ld = gu.data_ptr(), _rows(gu, "gu", dev, dh.dtype, R, 2 * inner)
+    else:
+        fmt = _sf_format(gu_sf, "gu_sf")
+        at = _codes_at(gu_codes, gu_sf, "gu_", dev, R, 2 * inner, fmt)
+    if out is None:
+        out = torch.empty(R, 2 * inner, dtype=dh.dtype, device=dh.device)
+    _check(ops_lib().moe_swiglu_bwd(
+        R, inner, dt, dh.data_ptr(), _rows(dh, "dh", dev, dh.dtype, R, inner), gu_at, gu_ld, *at, fmt, clamp,
+        None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), _used(offsets, dev),
+        out.data_ptr(), _rows(out, "out", dev, dh.dtype, R, 2 * inner), _raw_stream(dev)), "moe_swiglu_bwd")
+    if given is not None:
+        _wrote((given,))
+    return out
