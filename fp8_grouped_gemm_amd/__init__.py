@@ -387,5 +387,6 @@ _OPS_NAMES = ("moe_permute", "moe_permute_bwd", "moe_unpermute", "moe_unpermute_
               "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4",
               "moe_gemm_mxfp4_info", "moe_gate", "moe_gate_bwd", "moe_rms_norm", "moe_rms_norm_bwd",
               "moe_rms_norm_bwd_workspace_bytes", "moe_swiglu", "moe_swiglu_bwd",
+              "moe_gemm_wgrad", "moe_gemm_wgrad_workspace_bytes",
               "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SF_F32_128", "MOE_SF_UE8M0_32",
               "MOE_DTYPE_BF16", "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_U8")

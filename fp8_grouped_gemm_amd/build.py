@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libmoe_fp8.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["moe_api.cpp", "route.hip", "gemm_direct.hip", "gemm_lds.hip", "gemm_lds160.hip", "gemm_sa.hip",
            "gemm_mx.hip", "pack.hip", "quant.hip", "ops_api.cpp", "rows.hip", "mxfp4.hip",
-           "gemm_mxfp4.hip", "gate.hip", "norm.hip", "swiglu.hip"]
+           "gemm_mxfp4.hip", "gate.hip", "norm.hip", "swiglu.hip", "gemm_wgrad.hip"]
 PEAKS_LIB = os.path.join(HERE, "libmoe_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]
 

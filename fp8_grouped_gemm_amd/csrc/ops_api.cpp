@@ -193,6 +193,21 @@ int check_swiglu(int32_t R, int32_t inner, int32_t dtype, bool codes, int32_t fo
     return MOE_OK;
 }
 
+int check_wgrad(int32_t groups, int32_t rows, int32_t n, int32_t k)
+{
+    if (groups < 1 || rows < 0 || n < 0 || k < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (k % 32 != 0 || k > (1 << 20) || groups > 1024 || rows >= (1 << 28) || n >= (1 << 20))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+size_t wgrad_workspace(int32_t groups, int32_t rows, int32_t n, int32_t k)
+{
+    const int split = rows > 0 && n > 0 ? moe::wgrad_split(groups, rows, n, k) : 1;
+    return split > 1 ? static_cast<size_t>(split) * groups * n * k * 4 : 0;
+}
+
 int check_gemm(int32_t groups, int32_t rows, int32_t n, int32_t k)
 {
     if (groups < 1 || rows < 0 || n < 0 || k < 1)
@@ -389,7 +404,7 @@ int moe_gate(int32_t T, int32_t E, int32_t K, int32_t dtype, const void* logits,
     if (rc != MOE_OK)
         return rc;
     if (groups < 1 || E % groups != 0 || top_groups < 1 || top_groups > groups || group_top < 1 ||
-        group_top > E / groups || K > E / groups * top_groups || (groups == 1 && group_top != 1))
+        group_top > E / groups || K > E / groups * top_groups)
         return MOE_ERR_INVALID_ARG;
     if (groups > 64)
         return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -659,6 +674,70 @@ int moe_swiglu_bwd(int32_t R, int32_t inner, int32_t dtype, const void* dh, int6
     a.sf_format = sf_format;
     a.dgu = static_cast<char*>(dgu); a.dgu_ld = old * es;
     return launched(moe::launch_swiglu_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_gemm_wgrad(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t dtype,
+                   const void* dy, int64_t dy_ld, const uint8_t* x, const void* x_sf,
+                   int32_t sf_format, const int32_t* offsets, const int32_t* counts,
+                   int32_t accumulate, void* dw, int32_t dw_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream)
+{
+    const int ds = elem_bytes(dw_dtype);
+    int64_t sf_row;
+    int sf_align;
+    if ((dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) || ds < 2 ||
+        !sf_layout(sf_format, k, sf_row, sf_align) || (!offsets && (groups != 1 || counts)))
+        return MOE_ERR_INVALID_ARG;
+    int rc = check_wgrad(groups, rows, n, k);
+    if (rc != MOE_OK)
+        return rc;
+    if (k % sf_block(sf_format) != 0)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (n == 0 || (rows == 0 && accumulate))
+        return MOE_OK;
+    const int64_t ld = stride(dy_ld, n);
+    if (!dw || ld < 0 || (rows > 0 && (!dy || !x || !x_sf)) || misaligned(dy, 2) || misaligned(x, 16) ||
+        misaligned(x_sf, sf_align) || misaligned(dw, ds) || misaligned(workspace, 16) ||
+        misaligned(offsets, 4) || misaligned(counts, 4))
+        return MOE_ERR_INVALID_ARG;
+    const size_t need = wgrad_workspace(groups, rows, n, k);
+    if (need > 0 && !workspace)
+        return MOE_ERR_INVALID_ARG;
+    if (need > workspace_bytes)
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const int64_t cells = static_cast<int64_t>(groups) * n;
+    const Span out[2] = {span(dw, cells, k, k, ds), span(need ? workspace : nullptr, 1, need, need, 1)};
+    const Span in[5] = {span(dy, rows, ld, n, 2), span(x, rows, k, k, 1), span(x_sf, rows, sf_row, sf_row, 1),
+                        span(offsets, 1, groups + 1, groups + 1, 4), span(counts, 1, groups, groups, 4)};
+    const unsigned allowed[2] = {};
+    if (any_overlap(out, in, allowed))
+        return MOE_ERR_INVALID_ARG;
+    rc = moe::device_status();
+    if (rc != MOE_OK)
+        return rc;
+    moe::WgradArgs a{};
+    a.E = groups; a.R = rows; a.N = n; a.K = k;
+    a.dtype = dtype; a.dw_dtype = dw_dtype;
+    a.dy = static_cast<const char*>(dy); a.dy_ld = ld * 2;
+    a.x = x;
+    a.x_sf = static_cast<const char*>(x_sf);
+    a.sf_format = sf_format;
+    a.offsets = offsets; a.counts = counts;
+    a.accumulate = accumulate != 0;
+    a.dw = static_cast<char*>(dw);
+    a.partial = static_cast<float*>(workspace);
+    a.split = need > 0 ? moe::wgrad_split(groups, rows, n, k) : 1;
+    return launched(moe::launch_gemm_wgrad(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_gemm_wgrad_workspace_bytes(int32_t groups, int32_t rows, int32_t n, int32_t k, size_t* bytes)
+{
+    if (!bytes)
+        return MOE_ERR_INVALID_ARG;
+    const int rc = check_wgrad(groups, rows, n, k);
+    if (rc == MOE_OK)
+        *bytes = wgrad_workspace(groups, rows, n, k);
+    return rc;
 }
 
 }  // extern "C"

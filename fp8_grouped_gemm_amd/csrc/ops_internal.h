@@ -100,6 +100,22 @@ struct SwigluArgs {
     int64_t dgu_ld;
 };
 
+struct WgradArgs {
+    int32_t E, R, N, K;
+    int32_t dtype, dw_dtype;
+    const char* dy;
+    int64_t dy_ld;             // bytes
+    const uint8_t* x;
+    const char* x_sf;
+    int32_t sf_format;         // MOE_SF_*
+    const int32_t* offsets;    // null: dense
+    const int32_t* counts;     // may be null
+    bool accumulate;
+    char* dw;
+    float* partial;            // [split, E, N, K], split > 1
+    int32_t split;             // workgroups that share a tile's rows
+};
+
 hipError_t launch_gate(const GateArgs& a, hipStream_t s);
 hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t s);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
@@ -108,6 +124,9 @@ hipError_t launch_rms_norm_bwd(const NormArgs& a, hipStream_t s);
 int norm_partials(int rows, int width);
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
 hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t s);
+// The split of a call (host only).
+int wgrad_split(int groups, int rows, int n, int k);
+hipError_t launch_gemm_wgrad(const WgradArgs& a, hipStream_t s);
 hipError_t launch_permute(const RowsArgs& a, hipStream_t s);
 hipError_t launch_unpermute(const RowsArgs& a, hipStream_t s);  // also permute's gradient
 hipError_t launch_unpermute_bwd(const RowsArgs& a, hipStream_t s);

@@ -2,7 +2,7 @@
 order and back with their gradients, microscaled 4-bit quantisation, the
 product of two microscaled 4-bit matrices, and around the experts' products the
 router's choice, the residual norm and SwiGLU with 8-bit rows, each with its
-gradient.
+gradient, and the experts' weight gradients from 8-bit rows.
 
 One function per entry point.  Tensors are checked here (type, shape, layout,
 device), before the library's own checks; outputs are allocated where none
@@ -34,10 +34,12 @@ EXPORTED_SYMBOLS = (
     "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4", "moe_gemm_mxfp4_info",
     "moe_gate", "moe_gate_bwd", "moe_rms_norm", "moe_rms_norm_bwd",
     "moe_rms_norm_bwd_workspace_bytes", "moe_swiglu", "moe_swiglu_bwd",
+    "moe_gemm_wgrad", "moe_gemm_wgrad_workspace_bytes",
 )
 
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
            torch.float32: MOE_DTYPE_F32}
+_DTYPES_16 = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 _DTYPES_U8 = {**_DTYPES, torch.uint8: MOE_DTYPE_U8}
 
 _ops = None
@@ -68,6 +70,8 @@ def ops_lib():
         L.moe_rms_norm_bwd_workspace_bytes.argtypes = [i32, i32, vp]
         L.moe_swiglu.argtypes = [i32] * 3 + [vp, i64, f32, vp, vp, vp, i64] + [vp] * 4 + [i32, vp]
         L.moe_swiglu_bwd.argtypes = [i32] * 3 + [vp, i64, vp, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]
+        L.moe_gemm_wgrad.argtypes = ([i32] * 5 + [vp, i64, vp, vp, i32, vp, vp, i32, vp, i32, vp, size, vp])
+        L.moe_gemm_wgrad_workspace_bytes.argtypes = [i32] * 4 + [vp]
         for name in EXPORTED_SYMBOLS:
             getattr(L, name).restype = ctypes.c_int
         _ops = L
@@ -662,6 +666,69 @@ def moe_swiglu_bwd(dh, gu=None, gu_codes=None, gu_sf=None, row_src=None, offsets
         R, inner, dt, dh.data_ptr(), _rows(dh, "dh", dev, dh.dtype, R, inner), gu_at, gu_ld, *at, fmt, clamp,
         None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), _used(offsets, dev),
         out.data_ptr(), _rows(out, "out", dev, dh.dtype, R, 2 * inner), _raw_stream(dev)), "moe_swiglu_bwd")
+    if given is not None:
+        _wrote((given,))
+    return out
+
+
+def moe_gemm_wgrad_workspace_bytes(groups, rows, n, k):
+    """Bytes of workspace that a moe_gemm_wgrad call of these sizes needs."""
+    _int32("sizes", max(map(abs, (groups, rows, n, k))))
+    size = ctypes.c_size_t()
+    _check(ops_lib().moe_gemm_wgrad_workspace_bytes(groups, rows, n, k, ctypes.addressof(size)),
+           "moe_gemm_wgrad_workspace_bytes")
+    return size.value
+
+
+def moe_gemm_wgrad(dy, x, x_sf, offsets=None, counts=None, dtype=None, out=None, accumulate=False,
+                   workspace=None, stream=None):
+    """Weight gradients from 8-bit rows: dw [N, K] = dy^T x of dy [R, N] (bf16 or f16) and
+    x [R, K] e4m3 with x_sf (f32 per 128 columns or UE8M0 per 32), or dw [E, N, K] with
+    offsets int32 [E+1] and counts int32 [E] (None: the segments' whole lengths), each
+    expert's from its rows, zeros for one without.  dw's type: out's, else dtype,
+    else f32.  accumulate: out is added to.  workspace uint8, at least
+    moe_gemm_wgrad_workspace_bytes (None: allocated)."""
+    if not _here(dy, stream):
+        return _elsewhere(moe_gemm_wgrad, dy, stream, dy, x, x_sf, offsets, counts, dtype, out, accumulate,
+                          workspace)
+    dev, i32 = dy.get_device(), torch.int32
+    dt, R, N = _matrix(dy, "dy", _DTYPES_16)
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [rows, k]")
+    if offsets is None and counts is not None:
+        raise ValueError("counts without offsets")
+    if accumulate and out is None:
+        raise ValueError("accumulate without out")
+    K = x.shape[1]
+    E = 1
+    if offsets is not None:
+        E = offsets.numel() - 1
+        if E < 1:
+            raise ValueError(f"offsets: {E + 1} entries")
+    _int32("sizes", max(E, K))
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype {dtype}")
+    shape = (N, K) if offsets is None else (E, N, K)
+    given, fmt = out, _sf_format(x_sf, "x_sf")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dy.device)
+    elif out.requires_grad and torch.is_grad_enabled():
+        _lost("out")
+    x_at, sf_at = _codes_at(x, x_sf, "x_", dev, R, K, fmt)
+    need = moe_gemm_wgrad_workspace_bytes(E, R, N, K)
+    ws_at, ws_bytes = None, 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
+        ws_bytes = workspace.numel()
+        ws_at = _dense(workspace, "workspace", dev, torch.uint8, ws_bytes)
+    _check(ops_lib().moe_gemm_wgrad(
+        E, R, N, K, dt, dy.data_ptr(), _rows(dy, "dy", dev, dy.dtype, R, N), x_at, sf_at, fmt,
+        None if offsets is None else _dense(offsets, "offsets", dev, i32, E + 1),
+        None if counts is None else _dense(counts, "counts", dev, i32, E), bool(accumulate),
+        _dense(out, "out", dev, dtype, shape), _DTYPES[dtype], ws_at, ws_bytes, _raw_stream(dev)), "moe_gemm_wgrad")
     if given is not None:
         _wrote((given,))
     return out

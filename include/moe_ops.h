@@ -15,7 +15,8 @@
  *     rows' type and in 8 bits, with the gradients;
  *   - moe_swiglu: the activation between the experts' two products, in the rows'
  *     type and in 8 bits, with an 8-bit copy of its input and the gradient
- *     that reads that copy.
+ *     that reads that copy;
+ *   - moe_gemm_wgrad: the experts' weight gradients from rows kept in 8 bits.
  *
  * Conventions as in moe_fp8.h: device pointers owned by the caller, no
  * allocation, no host synchronisation, work enqueued on `stream` of the
@@ -187,7 +188,7 @@ int moe_gemm_mxfp4_info(int32_t groups, int32_t rows, int32_t n, int32_t k, int3
  * NaN, and with softmax or renorm the token's.
  *   logits   [T, E]  bf16, f16 or f32, row stride logits_ld
  *   bias     f32 [E], may be null;  mask uint8 [T], may be null
- *   score    MOE_SCORE_*;  groups 1: none (top_groups and group_top are then 1)
+ *   score    MOE_SCORE_*;  groups 1: none (top_groups is then 1, group_top without effect)
  *   topk_idx int32 [T, K], topk_w f32 [T, K]: what moe_forward and moe_route take
  * 1 <= E <= 1024, 1 <= K <= 64, K <= E / groups * top_groups, E % groups == 0,
  * groups <= 64, group_top <= E / groups, T < 2^28.  T == 0 is a no-op.  Outputs
@@ -266,8 +267,8 @@ int moe_rms_norm_bwd_workspace_bytes(int32_t rows, int32_t width, size_t* bytes)
  *   row_src  int32 [pool_rows], moe_route's: rows with an entry < 0 are padding; null: none
  *   used     int32 [1]: pool rows in use (moe_route's offsets + E); null: all
  *   h        [pool_rows, inner] in dtype, rounded once from f32; null: not written
- *   h_codes, h_sf    h in 8 bits, from the f32 values: the second product's rows;
- *                    null: not written
+ *   h_codes, h_sf    h in 8 bits, from the f32 values: the second product's rows, and what
+ *                    moe_gemm_wgrad takes for its weights; null: not written
  *   gu_codes, gu_sf  gu (not clamped) in 8 bits [pool_rows, 2 inner]: what
  *                    moe_swiglu_bwd needs, at half of gu's bytes or less; null: not written
  * Padding rows and rows from *used on are not read, and left as they were in every
@@ -293,6 +294,32 @@ int moe_swiglu_bwd(int32_t pool_rows, int32_t inner, int32_t dtype, const void* 
                    const void* gu, int64_t gu_ld, const uint8_t* gu_codes, const void* gu_sf,
                    int32_t sf_format, float clamp, const int32_t* row_src, const int32_t* used,
                    void* dgu, int64_t dgu_ld, void* stream);
+
+/*
+ * Weight gradients from rows kept in 8 bits:
+ *   dw[e, i, k] = sum over the rows r of expert e of dy[r, i] * x[r, k]
+ *   dy     [rows, n] bf16 or f16 (dtype), row stride dy_ld
+ *   x      uint8 [rows, k] e4m3, x_sf by sf_format: x[r, k] = code * scale, rounded to dy's
+ *          type (exact in bf16 with UE8M0 scales above its subnormals)
+ *   dw     [groups, n, k] bf16, f16 or f32 (dw_dtype), densely packed, rounded once from f32
+ * Segments as in moe_gemm_mxfp4: offsets null: dense, groups 1, every row; else
+ * expert e's rows are offsets[e] .. offsets[e] + counts[e] - 1 (counts null: up to
+ * offsets[e + 1]), cut at `rows`; rows outside are not read.  An expert without rows gets
+ * zeros.  accumulate: dw is added to (the stored value plus the f32 sum, rounded once) in
+ * place of overwritten; an expert without rows keeps its values.
+ * workspace holds moe_gemm_wgrad_workspace_bytes of these sizes (0 for most: null then;
+ * the rows of few experts are split over workgroups, whose sums meet there in a fixed order).
+ * k % 32 == 0 (MOE_SF_F32_128: % 128), 1 <= k <= 2^20, groups <= 1024, rows < 2^28,
+ * n < 2^20.  x and workspace 16-byte aligned, x_sf 4-byte (UE8M0: any).
+ * Outputs overlap nothing.  Equal calls give equal bits.
+ */
+int moe_gemm_wgrad(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t dtype,
+                   const void* dy, int64_t dy_ld, const uint8_t* x, const void* x_sf,
+                   int32_t sf_format, const int32_t* offsets, const int32_t* counts,
+                   int32_t accumulate, void* dw, int32_t dw_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+int moe_gemm_wgrad_workspace_bytes(int32_t groups, int32_t rows, int32_t n, int32_t k,
+                                   size_t* bytes);
 
 #ifdef __cplusplus
 }

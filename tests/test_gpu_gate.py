@@ -17,7 +17,7 @@ SHAPES = [
     (1, 1, 1, 1, 1, 1), (1, 384, 6, 1, 1, 1), (5, 2, 2, 1, 1, 1), (7, 63, 8, 1, 1, 1), (9, 64, 8, 8, 4, 2),
     (33, 65, 3, 5, 2, 1), (4, 65, 13, 13, 3, 5), (130, 256, 8, 8, 4, 2), (17, 257, 12, 1, 1, 1), (6, 300, 30, 60, 20, 3),
     (64, 384, 6, 64, 9, 2), (3, 512, 64, 4, 1, 100), (10, 1000, 10, 10, 5, 2), (5, 1024, 64, 64, 64, 16),
-    (3, 1024, 8, 1, 1, 1), (12, 6, 6, 6, 6, 1), (1025, 16, 2, 4, 1, 1),
+    (3, 1024, 8, 1, 1, 1), (12, 6, 6, 6, 6, 1), (8, 40, 4, 1, 1, 3), (1025, 16, 2, 4, 1, 1),
 ]
 
 
@@ -243,7 +243,8 @@ def test_binding_refusals():
         with pytest.raises(ValueError):
             f()
     for f in (lambda: moe.moe_gate(l, 0), lambda: moe.moe_gate(l, -1), lambda: moe.moe_gate(l, 33), lambda: moe.moe_gate(l, 2, groups=5),
-              lambda: moe.moe_gate(l, 2, group_top=2), lambda: moe.moe_gate_bwd(l, i, w, out=l)):
+              lambda: moe.moe_gate(l, 2, group_top=33), lambda: moe.moe_gate(l, 2, top_groups=2),
+              lambda: moe.moe_gate_bwd(l, i, w, out=l)):
         with pytest.raises(moe.MoEError):
             f()
     with torch.no_grad():

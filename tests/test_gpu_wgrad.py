@@ -1,0 +1,236 @@
+"""moe_gemm_wgrad on the GPU against plain float64 forms."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_grouped_gemm_amd as moe
+import layer_util as lu
+import ops_util as ou
+from parity_util import say
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+# rows, experts (0: dense), n, k, alignment: tiles and their edges, experts without rows, shares of rows
+SHAPES = [(1, 0, 1, 32, 1), (31, 0, 7, 96, 1), (32, 0, 128, 128, 1), (33, 0, 129, 160, 1), (200, 0, 40, 384, 1),
+          (5, 8, 33, 64, 1), (64, 3, 127, 256, 16), (300, 8, 136, 640, 1), (77, 1, 257, 128, 64), (1000, 5, 264, 288, 16),
+          (3000, 0, 50, 128, 1), (2500, 2, 130, 96, 8), (9000, 0, 300, 256, 1), (700, 40, 16, 128, 128), (513, 0, 512, 512, 1)]
+
+
+def x_values(codes, sf, dtype):
+    """What the codes stand for in dy's type: a float32 product, rounded."""
+    c = torch.from_numpy(lu.E4M3[codes.cpu().numpy()]).float()
+    s = torch.from_numpy(lu.scales(sf)).float()
+    return (c * s.repeat_interleave(codes.shape[1] // s.shape[1], 1)).to(dtype)
+
+
+def make(shape, dtype, fmt, seed=0):
+    """dy, codes, sf and lists (None: dense) of a pool whose padding rows are NaN."""
+    rows, E, n, k, align = shape
+    rng = np.random.default_rng(seed + rows + 3 * n + k)
+    lists = None
+    R = rows
+    if E:
+        idx = rng.integers(0, E, (rows, 1))
+        idx[idx == E // 2] = 0 if E > 1 else E // 2           # an expert without rows
+        lists = ou.route(idx, E, align)
+        R = lists["pool"]
+    dy = torch.from_numpy(rng.standard_normal((R, n))).to(dtype)
+    codes, sf = lu.quantised(torch.from_numpy(rng.standard_normal((R, k)) * (1 + 9 * (rng.random((1, k)) < 0.05))).float(), fmt)
+    if lists is not None:
+        dead = torch.from_numpy(lists["row_src"] < 0)
+        dy[dead] = float("nan")
+        codes[dead] = 0x7F
+    return dy, codes, sf, lists
+
+
+def plain(dy, xv, lists, E, whole=False):
+    """(sums, sums of magnitudes, most rows of an expert) in float64."""
+    dy, xv = lu.f64(dy), lu.f64(xv)
+    out, mag, most = [], [], 0
+    for e in range(max(1, E)):
+        a, m = (0, dy.shape[0]) if not E else (lists["offsets"][e], lists["counts"][e])
+        if E and whole:
+            m = lists["offsets"][e + 1] - a
+        out.append(dy[a:a + m].T @ xv[a:a + m])
+        mag.append(abs(dy[a:a + m]).T @ abs(xv[a:a + m]))
+        most = max(most, m)
+    return (out[0], mag[0], most) if not E else (np.stack(out), np.stack(mag), most)
+
+
+def bound_of(want, mag, most, dtype):
+    # exact products; each of the sum's `most` additions, and those of 16 shares, cut or rounded to 24 bits
+    return lu.rounded_bound(want, (most + 18) * 2.0 ** -23 * mag, dtype)
+
+
+def seg(lists):
+    return {} if lists is None else {k: torch.from_numpy(lists[k]).cuda() for k in ("offsets", "counts")}
+
+
+@pytest.mark.parametrize("fmt", [0, 1], ids=["f32", "ue8m0"])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_product_against_the_plain_form(shape, dtype, fmt):
+    if shape[3] % lu.BLOCK[fmt]:
+        pytest.skip("columns are no whole blocks")
+    say(f"weight gradient {shape} {dtype} {fmt}")
+    dt = DT[dtype]
+    dy, codes, sf, lists = make(shape, dt, fmt)
+    want, mag, most = plain(dy, x_values(codes, sf, dt), lists, shape[1])
+    d = (dy.cuda(), codes.cuda(), sf.cuda())
+    got = moe.moe_gemm_wgrad(*d, **seg(lists))
+    assert got.dtype == torch.float32
+    lu.within(got, want, bound_of(want, mag, most, torch.float32))
+    for out in (torch.bfloat16, torch.float16):
+        v = moe.moe_gemm_wgrad(*d, dtype=out, **seg(lists))
+        assert torch.equal(v, got.to(out))                    # the same sum, rounded once
+    again = moe.moe_gemm_wgrad(*d, **seg(lists))
+    assert torch.equal(again, got)
+    # added to what is there, experts without rows left as they were
+    for out in (torch.float32, torch.bfloat16):
+        old = torch.randn(got.shape, device="cuda").to(out)
+        v = moe.moe_gemm_wgrad(*d, out=old.clone(), accumulate=True, **seg(lists))
+        assert torch.equal(v, (old.float() + got).to(out))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_whole_numbers_are_exact(dtype):
+    # values and sums that float32 holds: every layout mistake shows, no rounding does
+    say("whole numbers")
+    dt = DT[dtype]
+    for rows, E, n, k in ((257, 0, 333, 480), (700, 6, 200, 224), (4100, 0, 65, 96)):
+        rng = np.random.default_rng(n)
+        idx = rng.integers(0, max(1, E), (rows, 1))
+        lists = ou.route(idx, E, 8) if E else None
+        R = lists["pool"] if E else rows
+        dy = torch.from_numpy(rng.integers(-8, 9, (R, n))).to(dt)
+        codes = torch.from_numpy(rng.integers(0, 256, (R, k)).astype(np.uint8))
+        codes[(codes & 127) == 127] = 0
+        codes = torch.where((codes & 120) >= 64, codes & 0xBF, codes)      # magnitudes below 4
+        sf = torch.from_numpy(rng.integers(127, 130, (R, k // 32)).astype(np.uint8))
+        want = plain(dy, x_values(codes, sf, dt), lists, E)[0]
+        got = moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda(), **seg(lists))
+        # (multiples of 2^-9 below 2^7 * rows in all: 24 bits hold 2^15, so sums of up to 200 rows or so;
+        # longer ones round, each addition to 2^-24 of at most the magnitudes)
+        m = plain(dy, x_values(codes, sf, dt), lists, E)[1]
+        lu.within(got, want, np.where(m * 512 < 2 ** 24, 0.0, m * (rows + 18) * 2.0 ** -23))
+
+
+def test_segments_without_counts_and_bad_lists():
+    say("segments")
+    shape = (200, 4, 70, 64, 16)
+    dy, codes, sf, lists = make(shape, torch.bfloat16, 1, 5)
+    dy, codes = torch.nan_to_num(dy, nan=0.5), torch.where(codes == 0x7F, 0x38, codes)
+    xv = x_values(codes, sf, torch.bfloat16)
+    off = torch.from_numpy(lists["offsets"]).cuda()
+    d = (dy.cuda(), codes.cuda(), sf.cuda())
+    want, mag, most = plain(dy, xv, lists, 4, whole=True)
+    lu.within(moe.moe_gemm_wgrad(*d, offsets=off), want, bound_of(want, mag, most, torch.float32))
+    # cut at the rows there are; an empty or negative length is no rows
+    R = dy.shape[0]
+    bad_off = torch.tensor([0, R - 5, R + 50, 7, 7], dtype=torch.int32).cuda()
+    counts = torch.tensor([3, 100, 4, -2], dtype=torch.int32).cuda()
+    got = moe.moe_gemm_wgrad(*d, offsets=bad_off, counts=counts)
+    for e, rows in enumerate((slice(0, 3), slice(R - 5, R), slice(0, 0), slice(0, 0))):
+        w, m, n = plain(dy[rows], xv[rows], None, 0)
+        lu.within(got[e], w, bound_of(w, m, n, torch.float32))
+    for kw in (dict(offsets=off, counts=torch.zeros_like(counts)), dict(offsets=torch.zeros_like(off))):
+        old = torch.full((4, 70, 64), 3.0, device="cuda")
+        assert torch.all(moe.moe_gemm_wgrad(*d, out=old.clone(), **kw) == 0)
+        assert torch.equal(moe.moe_gemm_wgrad(*d, out=old.clone(), accumulate=True, **kw), old)
+
+
+def test_strides_and_odd_addresses():
+    say("weight gradient strides")
+    for n in (64, 71, 130):
+        dy, codes, sf, _ = make((90, 0, n, 96, 1), torch.float16, 1, 2)
+        big = torch.full((90, n + 5), float("nan"), dtype=torch.float16, device="cuda")
+        big[:, 3:3 + n] = dy.cuda()
+        want = moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda())
+        assert torch.equal(moe.moe_gemm_wgrad(big[:, 3:3 + n], codes.cuda(), sf.cuda()), want)
+        odd = torch.zeros(n * 96 + 1, dtype=torch.bfloat16, device="cuda")
+        moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda(), out=odd[1:].view(n, 96))
+        assert torch.equal(odd[1:].view(n, 96), want.bfloat16()) and odd[0] == 0
+
+
+def test_special_values():
+    say("weight gradient: infinities and NaN")
+    dy, codes, sf, _ = make((50, 0, 40, 64, 1), torch.bfloat16, 1, 3)
+    dy[49, 3] = float("inf")
+    dy[10, 5] = float("nan")
+    codes[20, 7] = 0xFF
+    sf[30, 1] = 0xFF
+    codes[49, 8], codes[49, 9] = 0, 0x38
+    got = moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda()).cpu()
+    nan = torch.isnan(got)
+    want = torch.zeros(40, 64, dtype=torch.bool)
+    want[5], want[:, 7], want[:, 32:], want[3, 8] = True, True, True, True
+    assert torch.equal(nan | torch.isinf(got), want | (torch.arange(40) == 3)[:, None])
+    assert torch.all(nan[want & (torch.arange(40) != 3)[:, None]]) and got[3, 9] == float("inf") and nan[3, 8]
+    # a float32 result beyond f16 becomes an infinity
+    big = torch.full((8, 4), 3e4, dtype=torch.float16, device="cuda")
+    c, s = torch.full((8, 32), 0x48, dtype=torch.uint8, device="cuda"), torch.full((8, 1), 127, dtype=torch.uint8, device="cuda")
+    assert torch.all(moe.moe_gemm_wgrad(big, c, s, dtype=torch.float16) == float("inf"))
+    assert torch.all(moe.moe_gemm_wgrad(big, c, s) == 960000)
+    # x beyond f16's range rounds to an infinity of its type
+    s[:] = 127 + 15
+    assert torch.all(torch.isinf(moe.moe_gemm_wgrad(big, c, s)))
+
+
+def test_empty():
+    say("weight gradient: nothing to do")
+    e = torch.empty(0, 40, dtype=torch.bfloat16, device="cuda")
+    c, s = torch.empty(0, 64, dtype=torch.uint8, device="cuda"), torch.empty(0, 2, dtype=torch.uint8, device="cuda")
+    assert torch.all(moe.moe_gemm_wgrad(e, c, s, out=torch.ones(40, 64, device="cuda")) == 0)
+    assert torch.all(moe.moe_gemm_wgrad(e, c, s, out=torch.ones(40, 64, device="cuda"), accumulate=True) == 1)
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert torch.all(moe.moe_gemm_wgrad(e, c, s, offsets=off, out=torch.ones(3, 40, 64, device="cuda")) == 0)
+    none = torch.empty(5, 0, dtype=torch.bfloat16, device="cuda")
+    assert moe.moe_gemm_wgrad(none, torch.zeros(5, 64, dtype=torch.uint8, device="cuda"),
+                              torch.zeros(5, 2, dtype=torch.uint8, device="cuda")).shape == (0, 64)
+
+
+def test_rows_past_32_bit_offsets():
+    R, n, k = 600000, 4096, 4096                              # 4.9 GB of dy, 2.5 GB of codes
+    say(f"weight gradient of {R} rows")
+    dy = torch.zeros(R, n, dtype=torch.bfloat16, device="cuda")
+    codes, sf = torch.zeros(R, k, dtype=torch.uint8, device="cuda"), torch.full((R, k // 32), 127, dtype=torch.uint8, device="cuda")
+    tail = slice(R - 40, R)
+    dy[tail] = torch.randn(40, n, device="cuda").bfloat16()
+    codes[tail] = torch.randint(0, 0x7F, (40, k), device="cuda").to(torch.uint8)
+    off = torch.tensor([0, R - 40, R], dtype=torch.int32, device="cuda")
+    got = moe.moe_gemm_wgrad(dy, codes, sf, offsets=off)
+    assert torch.all(got[0] == 0)
+    want = moe.moe_gemm_wgrad(dy[tail].clone(), codes[tail].clone(), sf[tail].clone())
+    assert torch.equal(got[1], want)
+    del dy, codes, got
+    torch.cuda.empty_cache()
+
+
+def test_workspace_and_refusals():
+    say("weight gradient: refusals")
+    dy, codes, sf, _ = (t.cuda() if isinstance(t, torch.Tensor) else t for t in make((3000, 0, 50, 128, 1), torch.bfloat16, 1))
+    need = moe.moe_gemm_wgrad_workspace_bytes(1, 3000, 50, 128)
+    assert need > 0
+    want = moe.moe_gemm_wgrad(dy, codes, sf)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")      # NaN, whatever it holds
+    assert torch.equal(moe.moe_gemm_wgrad(dy, codes, sf, workspace=ws), want)
+    with pytest.raises(moe.MoEError) as e:
+        moe.moe_gemm_wgrad(dy, codes, sf, workspace=ws[:-16])
+    assert e.value.code == moe.MOE_ERR_WORKSPACE_TOO_SMALL
+    off = torch.tensor([0, 3000], dtype=torch.int32, device="cuda")
+    leaf = torch.zeros(50, 128, device="cuda", requires_grad=True)
+    bad = [lambda: moe.moe_gemm_wgrad(dy.float(), codes, sf), lambda: moe.moe_gemm_wgrad(dy.t(), codes, sf),
+           lambda: moe.moe_gemm_wgrad(dy[1:], codes, sf), lambda: moe.moe_gemm_wgrad(dy, codes.view(torch.int8), sf),
+           lambda: moe.moe_gemm_wgrad(dy, codes, sf.float()), lambda: moe.moe_gemm_wgrad(dy, codes, sf.half()),
+           lambda: moe.moe_gemm_wgrad(dy, codes, sf[:, :3]), lambda: moe.moe_gemm_wgrad(dy, codes, sf, counts=off),
+           lambda: moe.moe_gemm_wgrad(dy, codes, sf, offsets=off[:1]), lambda: moe.moe_gemm_wgrad(dy, codes, sf, offsets=off.long()),
+           lambda: moe.moe_gemm_wgrad(dy, codes, sf, offsets=off, counts=off), lambda: moe.moe_gemm_wgrad(dy, codes, sf, accumulate=True),
+           lambda: moe.moe_gemm_wgrad(dy, codes, sf, dtype=torch.float64), lambda: moe.moe_gemm_wgrad(dy, codes, sf, out=leaf),
+           lambda: moe.moe_gemm_wgrad(dy.clone().requires_grad_(), codes, sf), lambda: moe.moe_gemm_wgrad(dy, codes[0], sf),
+           lambda: moe.moe_gemm_wgrad(dy, codes, sf, out=want.t())]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    with torch.no_grad():
+        moe.moe_gemm_wgrad(dy, codes, sf, out=leaf)

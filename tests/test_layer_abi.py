@@ -1,5 +1,5 @@
 """The C ABI of the operators around the experts' products (moe_gate, moe_rms_norm,
-moe_swiglu and their gradients): every invalid call is refused on the host (CPU
+moe_swiglu and their gradients, moe_gemm_wgrad): every invalid call is refused on the host (CPU
 only: each call fails its checks before the device is queried, or is a no-op)."""
 import ctypes
 
@@ -28,6 +28,9 @@ SWIGLU = dict(R=4, inner=128, dtype=BF16, p_gu=X, gu_ld=0, clamp=0.0, p_row_src=
 SWIGLU_BWD = dict(R=4, inner=128, dtype=BF16, p_dh=X, dh_ld=0, p_gu=0, gu_ld=0, p_gc=Y, p_gsf=Y + 4096, fmt=0,
                   clamp=0.0, p_row_src=Z, p_used=Z + 4096, p_dgu=V, dgu_ld=0, p_stream=0)
 
+WGRAD = dict(groups=2, rows=64, n=48, k=128, dtype=BF16, p_dy=X, dy_ld=0, p_x=Y, p_sf=Z, fmt=0, p_off=V, p_counts=V + 64,
+             accumulate=0, p_dw=W, dw_dtype=F32, p_ws=U, ws_bytes=0, p_stream=0)
+
 
 def call(name, base, **change):
     a = {**base, **change}
@@ -40,7 +43,7 @@ def call(name, base, **change):
         (dict(dtype=-1), INV), (dict(score=2), INV), (dict(score=-1), INV), (dict(E=1032, groups=8), SHAPE),
         (dict(E=512, K=65), SHAPE), (dict(T=1 << 28), SHAPE), (dict(groups=0), INV), (dict(groups=7), INV),
         (dict(top_groups=0), INV), (dict(top_groups=9), INV), (dict(group_top=0), INV), (dict(group_top=9), INV),
-        (dict(K=17), INV), (dict(groups=1, top_groups=1), INV),
+        (dict(K=17), INV), (dict(groups=1, top_groups=2), INV), (dict(groups=1, top_groups=1, group_top=65), INV),
         (dict(E=130, groups=65, group_top=1), SHAPE), (dict(p_logits=0), INV), (dict(p_idx=0), INV),
         (dict(p_w=0), INV), (dict(p_logits=X + 1), INV), (dict(p_bias=Y + 2), INV), (dict(p_idx=V + 2), INV),
         (dict(p_w=W + 1), INV), (dict(ld=63), INV), (dict(ld=-1), INV), (dict(ld=(1 << 30) + 1), INV),
@@ -85,6 +88,19 @@ def call(name, base, **change):
         (dict(p_gu=W, p_gc=0, p_gsf=0, gu_ld=255), INV), (dict(p_gc=Y + 4), INV), (dict(p_dgu=V + 1), INV),
         (dict(p_dgu=X), INV), (dict(p_dgu=Y), INV), (dict(p_dgu=Z), INV),
         (dict(p_gu=V, gu_ld=300, p_gc=0, p_gsf=0), INV), (dict(p_gu=V + 2, p_gc=0, p_gsf=0), INV)]),
+    ("moe_gemm_wgrad", WGRAD, [
+        (dict(groups=0), INV), (dict(rows=-1), INV), (dict(n=-1), INV), (dict(k=0), INV), (dict(dtype=F32), INV),
+        (dict(dtype=U8), INV), (dict(dw_dtype=U8), INV), (dict(dw_dtype=5), INV), (dict(fmt=2), INV),
+        (dict(p_off=0), INV), (dict(p_off=0, groups=1), INV), (dict(k=96), SHAPE), (dict(k=48, fmt=1), SHAPE),
+        (dict(k=(1 << 20) + 128), SHAPE), (dict(groups=1025), SHAPE), (dict(rows=1 << 28), SHAPE),
+        (dict(n=1 << 20), SHAPE), (dict(p_dy=0), INV), (dict(p_x=0), INV), (dict(p_sf=0), INV), (dict(p_dw=0), INV),
+        (dict(dy_ld=47), INV), (dict(p_dy=X + 1), INV), (dict(p_x=Y + 8), INV), (dict(p_sf=Z + 2), INV),
+        (dict(p_dw=W + 2), INV), (dict(p_off=V + 1), INV), (dict(p_counts=V + 66), INV), (dict(p_ws=U + 8), INV),
+        (dict(p_dw=X), INV), (dict(p_dw=Y), INV), (dict(p_dw=Z + 4 * 60), INV), (dict(p_dw=V), INV),
+        (dict(p_dw=V + 64), INV),
+        (dict(groups=1, p_off=0, p_counts=0, rows=8192, ws_bytes=0), SMALL),
+        (dict(groups=1, p_off=0, p_counts=0, rows=8192, p_ws=0, ws_bytes=1 << 30), INV),
+        (dict(groups=1, p_off=0, p_counts=0, rows=8192, p_ws=W, ws_bytes=1 << 30), INV)]),
 ])
 def test_refusals(name, base, changes):
     for change, code in changes:
@@ -99,6 +115,8 @@ def test_empty_calls_are_no_ops():
     assert call("moe_rms_norm_bwd", NORM_BWD, rows=0, p_dw=0) == OK
     assert call("moe_swiglu", SWIGLU, R=0, p_gu=0, p_h=0) == OK
     assert call("moe_swiglu_bwd", SWIGLU_BWD, R=0, p_dh=0, p_dgu=0) == OK
+    assert call("moe_gemm_wgrad", WGRAD, n=0, p_dw=0) == OK
+    assert call("moe_gemm_wgrad", WGRAD, rows=0, accumulate=1, p_dw=0) == OK
     # what else is wrong with an empty call is still refused
     assert call("moe_gate", GATE, T=0, E=0) == INV
     assert call("moe_rms_norm", NORM, rows=0, width=200) == SHAPE
@@ -117,12 +135,21 @@ def test_workspace_query():
     with pytest.raises(ValueError, match="beyond 32 bits"):
         q((1 << 32) + 4, 4)
     assert ops.ops_lib().moe_rms_norm_bwd_workspace_bytes(4, 4, None) == INV
+    # weight gradients: nothing where tiles fill the card, bounded where rows are split
+    w = moe.moe_gemm_wgrad_workspace_bytes
+    assert w(32, 12288, 4096, 4096) == 0 and w(1, 0, 64, 64) == 0 and w(1, 100000, 0, 64) == 0
+    assert 0 < w(1, 1 << 20, 64, 64) <= 64 * 64 * 64 * 4 and w(1, 8192, 384, 7168) <= 16 * 384 * 7168 * 4
+    for bad, code in (((0, 4, 4, 32), INV), ((1, 4, 4, 48), SHAPE), ((1025, 4, 4, 32), SHAPE)):
+        with pytest.raises(moe.MoEError) as e:
+            w(*bad)
+        assert e.value.code == code
 
 
 def test_binding_refuses_host_tensors():
     x, i = torch.zeros(2, 256), torch.zeros(2, 2, dtype=torch.int32)
     for f in (lambda: moe.moe_gate(x, 2), lambda: moe.moe_gate_bwd(x, i, x[:, :2]), lambda: moe.moe_rms_norm(x),
               lambda: moe.moe_rms_norm_bwd(x, x, x[:, 0]), lambda: moe.moe_swiglu(x),
-              lambda: moe.moe_swiglu_bwd(x, gu=x)):
+              lambda: moe.moe_swiglu_bwd(x, gu=x),
+              lambda: moe.moe_gemm_wgrad(x.half(), x.to(torch.uint8), x[:, :8].to(torch.uint8))):
         with pytest.raises(ValueError, match="expected a GPU"):
             f()
