@@ -11,6 +11,8 @@ namespace {
 
 constexpr int64_t kMaxLd = INT64_C(1) << 30;  // row strides, elements (spans stay below 2^63 bytes)
 
+constexpr int64_t kMaxWgradLd = INT64_C(1) << 24;  // (a stage of 64 of dy's rows spans at most 2^31 bytes)
+
 // Bytes per element, 0 for an unknown type.
 int elem_bytes(int32_t dtype)
 {
@@ -696,7 +698,7 @@ int moe_gemm_wgrad(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
     if (n == 0 || (rows == 0 && accumulate))
         return MOE_OK;
     const int64_t ld = stride(dy_ld, n);
-    if (!dw || ld < 0 || (rows > 0 && (!dy || !x || !x_sf)) || misaligned(dy, 2) || misaligned(x, 16) ||
+    if (!dw || ld < 0 || ld > kMaxWgradLd || (rows > 0 && (!dy || !x || !x_sf)) || misaligned(dy, 2) || misaligned(x, 16) ||
         misaligned(x_sf, sf_align) || misaligned(dw, ds) || misaligned(workspace, 16) ||
         misaligned(offsets, 4) || misaligned(counts, 4))
         return MOE_ERR_INVALID_ARG;

@@ -48,6 +48,7 @@ struct Bf16 {
             r[i] = f32x2_to_bf16x2(f[2 * i], f[2 * i + 1]);
         return r;
     }
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) { return f32x2_to_bf16x2(a, b); }
     static __device__ __forceinline__ float load(const char* p)
     {
         return bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
@@ -84,6 +85,7 @@ struct F16 {
             r[i] = bits(f[2 * i]) | (bits(f[2 * i + 1]) << 16);
         return r;
     }
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) { return bits(a) | bits(b) << 16; }
     static __device__ __forceinline__ float load(const char* p)
     {
         return value(*reinterpret_cast<const uint16_t*>(p));

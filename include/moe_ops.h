@@ -298,7 +298,7 @@ int moe_swiglu_bwd(int32_t pool_rows, int32_t inner, int32_t dtype, const void* 
 /*
  * Weight gradients from rows kept in 8 bits:
  *   dw[e, i, k] = sum over the rows r of expert e of dy[r, i] * x[r, k]
- *   dy     [rows, n] bf16 or f16 (dtype), row stride dy_ld
+ *   dy     [rows, n] bf16 or f16 (dtype), row stride dy_ld, here at most 2^24
  *   x      uint8 [rows, k] e4m3, x_sf by sf_format: x[r, k] = code * scale, rounded to dy's
  *          type (exact in bf16 with UE8M0 scales above its subnormals)
  *   dw     [groups, n, k] bf16, f16 or f32 (dw_dtype), densely packed, rounded once from f32

@@ -94,7 +94,7 @@ def call(name, base, **change):
         (dict(p_off=0), INV), (dict(p_off=0, groups=1), INV), (dict(k=96), SHAPE), (dict(k=48, fmt=1), SHAPE),
         (dict(k=(1 << 20) + 128), SHAPE), (dict(groups=1025), SHAPE), (dict(rows=1 << 28), SHAPE),
         (dict(n=1 << 20), SHAPE), (dict(p_dy=0), INV), (dict(p_x=0), INV), (dict(p_sf=0), INV), (dict(p_dw=0), INV),
-        (dict(dy_ld=47), INV), (dict(p_dy=X + 1), INV), (dict(p_x=Y + 8), INV), (dict(p_sf=Z + 2), INV),
+        (dict(dy_ld=47), INV), (dict(dy_ld=(1 << 24) + 1), INV), (dict(p_dy=X + 1), INV), (dict(p_x=Y + 8), INV), (dict(p_sf=Z + 2), INV),
         (dict(p_dw=W + 2), INV), (dict(p_off=V + 1), INV), (dict(p_counts=V + 66), INV), (dict(p_ws=U + 8), INV),
         (dict(p_dw=X), INV), (dict(p_dw=Y), INV), (dict(p_dw=Z + 4 * 60), INV), (dict(p_dw=V), INV),
         (dict(p_dw=V + 64), INV),
