@@ -29,6 +29,8 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) rows_u32x4 lds_u32x4;
 
 constexpr int kMostSplit = 16;
 constexpr int kStrip = 8;
@@ -48,6 +50,18 @@ __device__ __forceinline__ v16f mfma(F16, const Frag& a, const Frag& b, const v1
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
+template <bool HI>
+__device__ __forceinline__ uint32_t scaled2(Bf16, uint32_t q, float scale)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)q, scale, HI));
+}
+
+template <bool HI>
+__device__ __forceinline__ uint32_t scaled2(F16, uint32_t q, float scale)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)q, scale, HI));
+}
+
 // Byte of element (row, col) of a stage's matrix of COLS 16-bit columns.
 template <int COLS>
 __device__ __forceinline__ int lds_at(int row, int col)
@@ -56,58 +70,77 @@ __device__ __forceinline__ int lds_at(int row, int col)
     return row * COLS * 2 + ((col * 2) ^ ((row & (kSlots - 1)) << 6));
 }
 
-// The 8 rows of column c0 + lane % 32 that the lane gives the matrix instruction:
-// r0 + 4 (lane / 32) .. + 3 and the same 8 rows on (the same set for both operands,
-// whose order the sum does not know).
+// Where in its row of LDS x's column c (a multiple of 16) lies: of each 64 columns the 32 even
+// ones first, then the odd ones.
+__device__ __forceinline__ int x_place(int c) { return (c & ~63) + (c & 63) / 2; }
+
+// Of the 8 rows of column c0 + lane % 32 that the lane gives the matrix instruction, the
+// byte where its first read starts: rows 4 (lane / 32) .. + 3, and the same 8 rows on
+// (the same set for both operands, whose order the sum does not know).
 template <int COLS>
-__device__ __forceinline__ Frag read_frag(char* lds, int r0, int c0, int lane)
+__device__ __forceinline__ int frag_at(int c0, int lane)
 {
-    const int row = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-    const int col = c0 + (lane & 16) + 4 * (lane & 3);
+    return lds_at<COLS>(4 * (lane >> 5) + ((lane & 15) >> 2), c0 + (lane & 16) + 4 * (lane & 3));
+}
+
+template <int COLS>
+__device__ __forceinline__ Frag read_frag(lds_char* at, int r0)
+{
     Frag f;
-    f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + lds_at<COLS>(row, col)));
-    f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + lds_at<COLS>(row + 8, col)));
+    f.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + r0 * COLS * 2));
+    f.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + (r0 + 8) * COLS * 2));
     return f;
 }
 
-// 16 codes times their scale, rounded to E: two pieces of eight values.
-template <class E>
-__device__ __forceinline__ void decode16(rows_u32x4 q, float scale, rows_u32x4* out)
+// 16 codes times their scale, rounded to E: the eight of even and the eight of odd columns.
+// A power of two in one instruction (equal to the product's rounding for every code and
+// scale code, 0 and 0xFF among them; f16 keeps the sign of -0).
+template <class E, bool MX>
+__device__ __forceinline__ void decode16(rows_u32x4 q, uint32_t sf, rows_u32x4* out)
 {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    float f[16];
+    const float scale = __uint_as_float(!MX ? sf : sf == 0 ? 0x400000u : sf == 0xFFu ? 0x7FC00000u : sf << 23);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
-        f[4 * i] = a[0] * scale;
-        f[4 * i + 1] = a[1] * scale;
-        f[4 * i + 2] = b[0] * scale;
-        f[4 * i + 3] = b[1] * scale;
-    }
-    out[0] = E::pack(f);
-    out[1] = E::pack(f + 8);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // bytes h, h + 2, h + 4, h + 6 of eight codes
+            const uint32_t c = __builtin_amdgcn_perm(q[2 * i + 1], q[2 * i], h ? 0x07050301u : 0x06040200u);
+            if constexpr (MX) {
+                out[h][2 * i] = scaled2<false>(E{}, c, scale);
+                out[h][2 * i + 1] = scaled2<true>(E{}, c, scale);
+            } else {
+                typedef float f2 __attribute__((ext_vector_type(2)));
+                const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
+                const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+                out[h][2 * i] = E::pack2(a[0] * scale, a[1] * scale);
+                out[h][2 * i + 1] = E::pack2(b[0] * scale, b[1] * scale);
+            }
+        }
 }
 
-// A buffer of `bytes` bytes, past whose end loads give zeros.
+// A buffer of `bytes` bytes, past whose end loads give zeros; p and bytes are the same in
+// every lane (said to the compiler, which else loops over the lanes' values).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, unsigned bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)u), hi = __builtin_amdgcn_readfirstlane((int)(u >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
 
 // First row and number of rows of a group's share `s` of S (whole stages but the last).
 __device__ __forceinline__ void share(const WgradArgs& a, int e, int s, int64_t& first, int& rows)
 {
-    int64_t lo = 0, hi = a.R;
+    int lo = 0, all = a.R;
     if (a.offsets) {
         lo = max(a.offsets[e], 0);
-        hi = a.counts ? lo + max(a.counts[e], 0) : (int64_t)a.offsets[e + 1];
-        hi = min(hi, (int64_t)a.R);
+        const int64_t hi = a.counts ? (int64_t)lo + max(a.counts[e], 0) : (int64_t)a.offsets[e + 1];
+        all = (int)max(min(hi, (int64_t)a.R) - lo, INT64_C(0));
     }
-    const int64_t all = max(hi - lo, INT64_C(0));
-    const int64_t per = ((all + a.split - 1) / a.split + kShareRows - 1) / kShareRows * kShareRows;
-    const int64_t at = min(per * s, all);
-    first = lo + at;
-    rows = (int)min(per, all - at);
+    const int per = ((all + a.split - 1) / a.split + kShareRows - 1) / kShareRows * kShareRows;
+    const int at = min(per * s, all);  // (rows are below 2^28, shares at most 16)
+    first = (int64_t)lo + at;
+    rows = min(per, all - at);
 }
 
 // One value to dw (type OUT), added to what is there with `add`.
@@ -119,64 +152,40 @@ __device__ __forceinline__ void put(char* p, float v, bool add)
     OUT::store(p, v);
 }
 
-// The neighbour lane's value.
-__device__ __forceinline__ uint32_t neighbour(uint32_t v) { return row_perm_u<0xB1>(v); }
-
-// A wave's blocks of dw: lane l holds column l % 32 and rows 8 (k / 4) + 4 (l / 32) + k % 4
-// of each.  16-bit types: neighbouring lanes first exchange one of two rows' values, so
-// that each has two adjacent columns of one row, then of two blocks' one, so that a store
-// writes whole lines of 128 bytes, as one of f32 does (64-byte runs: 2.6 TB/s for 5.4).
+// A wave's blocks of dw.  Lane l holds rows 8 (k / 4) + 4 (l / 32) + k % 4 of each and,
+// x's columns lying in LDS as they do, columns 2 (l % 32) of the first and 2 (l % 32) + 1 of
+// the second of two blocks: adjacent ones, which a store writes as whole lines (64-byte
+// runs of single columns: 2.6 TB/s for 5.4).
 template <class OUT, int MB, int NB>
 __device__ __forceinline__ void put_blocks(char* dw, const v16f (&acc)[MB][NB], int row0, int col0, int N, int K,
                                            int lane, bool add)
 {
-    const bool odd = lane & 1;
+    const bool inside = row0 + MB * 32 <= N && col0 + NB * 32 <= K;
+    char* const at = dw + ((int64_t)row0 * K + col0) * OUT::SIZE;
+    const unsigned lane_at = (4 * (lane >> 5) * (unsigned)K + 2 * (lane & 31)) * OUT::SIZE;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-            const int row = row0 + i * 32 + 8 * (k / 4) + 4 * (lane >> 5) + k % 4;
+        for (int k = 0; k < 16; ++k) {
+            const int r = i * 32 + 8 * (k / 4) + k % 4;
+            const bool in_row = inside || row0 + r + 4 * (lane >> 5) < N;
+            char* const row = at + (int64_t)r * K * OUT::SIZE;
 #pragma unroll
             for (int j = 0; j < NB; j += 2) {
+                if (!inside && !(in_row && col0 + j * 32 + 2 * (lane & 31) < K))
+                    continue;
+                char* const to = row + j * 32 * OUT::SIZE + lane_at;
+                float v[2] = {acc[i][j][k], acc[i][j + 1][k]};
+                if (add) {
+                    v[0] += OUT::load(to);
+                    v[1] += OUT::load(to + OUT::SIZE);
+                }
                 if constexpr (OUT::SIZE == 4) {
-                    const int col = col0 + j * 32 + (lane & 31);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        if (row + h / 2 < N && col + h % 2 * 32 < K)
-                            put<OUT>(dw + ((int64_t)(row + h / 2) * K + col + h % 2 * 32) * 4, acc[i][j + h % 2][k + h / 2], add);
+                    typedef float two __attribute__((ext_vector_type(2), aligned(4)));
+                    *reinterpret_cast<two*>(to) = (two){v[0], v[1]};
                 } else {
-                    // the lane's columns: two of block j (even lanes) or j + 1, of row and row + 1
-                    const int col = col0 + (j + odd) * 32 + (lane & 30);
-                    float v[2][2];  // [block][row], columns col % 32 and the next
-                    uint32_t two[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float lo = acc[i][j + b][k], hi = acc[i][j + b][k + 1];
-                        const float got = row_perm<0xB1>(odd ? lo : hi);
-                        v[b][0] = odd ? got : lo;
-                        v[b][1] = odd ? hi : got;
-                    }
-                    if (add) {  // block b of the lane's row is at its own place now
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int r = row + odd, c = col0 + (j + b) * 32 + (lane & 30);
-                            if (r < N && c < K) {
-                                const char* const at = dw + ((int64_t)r * K + c) * 2;
-                                v[b][0] += OUT::load(at);
-                                v[b][1] += OUT::load(at + 2);
-                            }
-                        }
-                    }
-                    two[0] = OUT::pack2(v[0][0], v[0][1]);
-                    two[1] = OUT::pack2(v[1][0], v[1][1]);
-                    const uint32_t got = neighbour(odd ? two[0] : two[1]);
-                    const uint32_t at_row = odd ? got : two[0], at_next = odd ? two[1] : got;
-                    typedef unsigned int bytes4 __attribute__((aligned(1)));
-                    char* const at = dw + ((int64_t)row * K + col) * 2;
-                    if (row < N && col < K)
-                        *reinterpret_cast<bytes4*>(at) = at_row;
-                    if (row + 1 < N && col < K)
-                        *reinterpret_cast<bytes4*>(at + (int64_t)K * 2) = at_next;
+                    typedef unsigned int two __attribute__((aligned(2)));
+                    *reinterpret_cast<two*>(to) = OUT::pack2(v[0], v[1]);
                 }
             }
         }
@@ -184,8 +193,8 @@ __device__ __forceinline__ void put_blocks(char* dw, const v16f (&acc)[MB][NB], 
 
 }  // namespace
 
-// A workgroup computes BM rows (dy's columns) by BN columns (x's) of one expert's dw
-// over one share of its rows; its waves WM by WN each.
+// A workgroup computes BM rows (dy's columns) by BN columns (x's) of an expert's dw over
+// one share of its rows, its waves WM by WN each; kStage rows at a time.
 template <class E, bool MX, int BM, int BN, int WM, int WN, int kStage>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(WgradArgs a, int tiles_m, int tiles_n)
 {
@@ -193,38 +202,49 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
     constexpr int kBytes = kStage * (BM + BN) * 2;  // of a stage in LDS
     constexpr int kDy = kStage * BM / 8 / kThreads, kX = kStage * BN / 16 / kThreads;  // pieces a thread loads
     static_assert(kDy >= 1 && kX >= 1 && kStage * BN / 16 % kThreads == 0, "whole pieces");
-    __shared__ __attribute__((aligned(16))) char lds[2][kBytes];
-
-    // Workgroups go to the 8 dies in turn: each die takes a run of a unit's (a share of an
-    // expert's) tiles, counted down strips of kStrip rows, so that it reads a compact block.
-    const unsigned wg = workgroup(), tiles = tiles_m * tiles_n, run = (tiles + 7) / 8;
-    const unsigned unit = wg / (run * 8), in = wg - unit * run * 8;
-    const unsigned tile = (in & 7) * run + in / 8;
-    if (unit >= (unsigned)(a.E * a.split) || tile >= tiles)
-        return;
-    const int e = unit / a.split, s = unit - e * a.split;
-    const int strip = tile / (kStrip * tiles_n), left = tile - strip * kStrip * tiles_n;
-    const int high = min(kStrip, tiles_m - strip * kStrip);
-    const int m0 = (strip * kStrip + left % high) * BM, n0 = left / high * BN;
+    static_assert(kThreads % (BM / 8) == 0, "a thread's pieces lie in the same columns of dy");
+    __shared__ __attribute__((aligned(16))) char stages_lds[2 * kBytes];
+    lds_char* const lds = (lds_char*)stages_lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
 
+    // Workgroups go to the 8 dies in turn.  Of every unit's (a share of an expert's) tiles, counted
+    // down strips of kStrip rows, a die takes a run: a compact block, whose rows and
+    // columns its L2 holds; the die that gets the last, shorter one changes from unit to
+    // unit.  Shares of one expert are equally long, so that the dies take runs of them all.
+    const unsigned tiles = tiles_m * tiles_n, die = workgroup() & 7, turn = workgroup() >> 3;
+    unsigned unit, tile;
+    if (a.E == 1) {
+        const unsigned all = tiles * a.split, at = die * ((all + 7) / 8) + turn;
+        unit = turn < (all + 7) / 8 && at < all ? at / tiles : a.split;
+        tile = at - unit * tiles;
+    } else {
+        const unsigned run = (tiles + 7) / 8;
+        unit = turn / run;
+        tile = ((die + unit) & 7) * run + turn - unit * run;
+    }
+    if (unit >= (unsigned)(a.E * a.split) || tile >= tiles)
+        return;
+    const int e = unit / a.split, s = unit - e * a.split;
+    const int strip = tile / (kStrip * tiles_n), in_strip = tile - strip * kStrip * tiles_n;
+    const int high = min(kStrip, tiles_m - strip * kStrip);
+    const int m0 = (strip * kStrip + in_strip % high) * BM, n0 = in_strip / high * BN;
     int64_t first;
     int rows;
     share(a, e, s, first, rows);
+    rows = __builtin_amdgcn_readfirstlane(rows);
     const int stages = (rows + kStage - 1) / kStage;
+    const int sf_row = MX ? a.K / 32 : a.K / 128 * 4;
     const char* const dy = a.dy + first * a.dy_ld;
     const uint8_t* const x = a.x + first * a.K;
-    const char* const sf = a.x_sf + first * (MX ? a.K / 32 : a.K / 128 * 4);
+    const char* const sf = a.x_sf + first * sf_row;
 
-    // The thread's pieces: offsets from a stage's first row, kOut for columns past the
+    // The thread's pieces of a stage: offsets from its first row, kOut for columns past the
     // matrix.  A buffer ends with the share's last row, so that rows past it (and kOut) read as
     // zeros; only a piece that holds a row's last columns and more is loaded one by one.
     constexpr unsigned kOut = 0x80000000u;
     unsigned d_at[kDy], x_at[kX], sf_at[kX];
-    int ragged = 0;  // columns of such a piece (the thread's pieces lie in the same columns)
-    const int sf_row = MX ? a.K / 32 : a.K / 128 * 4;
-    static_assert(kThreads % (BM / 8) == 0, "a thread's pieces lie in the same columns");
+    int ragged = 0;  // columns of such a piece
 #pragma unroll
     for (int p = 0; p < kDy; ++p) {
         const int piece = p * kThreads + threadIdx.x, c = m0 + piece % (BM / 8) * 8;
@@ -237,20 +257,21 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
         x_at[p] = c < a.K ? r * (unsigned)a.K + c : kOut;
         sf_at[p] = c < a.K ? r * (unsigned)sf_row + (MX ? c / 32 : c / 128 * 4) : kOut;
     }
-    const bool odd_edge = a.N % 8 != 0 && m0 + BM > a.N;
+    const bool cut_edge = a.N % 8 != 0 && m0 + BM > a.N;
     const auto bytes_left = [&](int r0, int64_t ld, int64_t width) {
         const int64_t n = (rows - r0 - 1) * ld + width;
-        return (unsigned)min(n, INT64_C(0x7FFFFFFF));
+        return r0 < rows ? (unsigned)min(n, INT64_C(0x7FFFFFFF)) : 0u;
     };
-
-    rows_u32x4 dreg[kDy], xreg[kX];
-    uint32_t xs[kX];
-    const auto load = [&](int stage) {
+    struct Regs {
+        rows_u32x4 dy[kDy], x[kX];
+        uint32_t sf[kX];
+    };
+    const auto load = [&](int stage, Regs& to) {
         const int r0 = stage * kStage;
         const auto db = buffer(dy + r0 * a.dy_ld, bytes_left(r0, a.dy_ld, a.N * 2));
         const auto xb = buffer(x + (int64_t)r0 * a.K, bytes_left(r0, a.K, a.K));
         const auto sb = buffer(sf + (int64_t)r0 * sf_row, bytes_left(r0, sf_row, sf_row));
-        if (odd_edge && ragged) {
+        if (cut_edge && ragged) {
 #pragma unroll
             for (int p = 0; p < kDy; ++p) {
                 const int r = r0 + (p * kThreads + (int)threadIdx.x) / (BM / 8);
@@ -261,44 +282,80 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
                                ? reinterpret_cast<const uint16_t*>(dy + r0 * a.dy_ld + d_at[p])[i] : 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    dreg[p][i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
+                    to.dy[p][i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
             }
         } else {
 #pragma unroll
             for (int p = 0; p < kDy; ++p)
-                dreg[p] = __builtin_bit_cast(rows_u32x4, __builtin_amdgcn_raw_buffer_load_b128(db, d_at[p], 0, 0));
+                to.dy[p] = __builtin_bit_cast(rows_u32x4, __builtin_amdgcn_raw_buffer_load_b128(db, d_at[p], 0, 0));
         }
 #pragma unroll
         for (int p = 0; p < kX; ++p) {
-            xreg[p] = __builtin_bit_cast(rows_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, x_at[p], 0, 0));
+            to.x[p] = __builtin_bit_cast(rows_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, x_at[p], 0, 0));
             if constexpr (MX)
-                xs[p] = __builtin_amdgcn_raw_buffer_load_b8(sb, sf_at[p], 0, 0);
+                to.sf[p] = __builtin_amdgcn_raw_buffer_load_b8(sb, sf_at[p], 0, 0);
             else
-                xs[p] = __builtin_amdgcn_raw_buffer_load_b32(sb, sf_at[p], 0, 0);
-        }
-    };
-    const auto store = [&](char* to) {
-#pragma unroll
-        for (int p = 0; p < kDy; ++p) {
-            const int piece = p * kThreads + threadIdx.x;
-            *reinterpret_cast<rows_u32x4*>(to + lds_at<BM>(piece / (BM / 8), piece % (BM / 8) * 8)) = dreg[p];
-        }
-        char* const xt = to + kStage * BM * 2;
-#pragma unroll
-        for (int p = 0; p < kX; ++p) {
-            const int piece = p * kThreads + threadIdx.x;
-            const int r = piece / (BN / 16), c = piece % (BN / 16) * 16;
-            rows_u32x4 v[2];
-            // code 0 is the subnormal 2^-127, 0xFF NaN
-            const uint32_t b = xs[p];
-            const uint32_t scale = !MX ? b : b == 0 ? 0x400000u : b == 0xFFu ? 0x7FC00000u : b << 23;
-            decode16<E>(xreg[p], __uint_as_float(scale), v);
-            *reinterpret_cast<rows_u32x4*>(xt + lds_at<BN>(r, c)) = v[0];
-            *reinterpret_cast<rows_u32x4*>(xt + lds_at<BN>(r, c + 8)) = v[1];
+                to.sf[p] = __builtin_amdgcn_raw_buffer_load_b32(sb, sf_at[p], 0, 0);
         }
     };
 
+    int d_to[kDy], x_to[kX][2];
+#pragma unroll
+    for (int p = 0; p < kDy; ++p) {
+        const int piece = p * kThreads + threadIdx.x;
+        d_to[p] = lds_at<BM>(piece / (BM / 8), piece % (BM / 8) * 8);
+    }
+#pragma unroll
+    for (int p = 0; p < kX; ++p) {
+        const int piece = p * kThreads + threadIdx.x;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            x_to[p][h] = kStage * BM * 2 + lds_at<BN>(piece / (BN / 16), x_place(piece % (BN / 16) * 16) + 32 * h);
+    }
+    const auto store = [&](int buf, const Regs& from) {
+#pragma unroll
+        for (int p = 0; p < kDy; ++p)
+            *(lds_u32x4*)(lds + buf + d_to[p]) = from.dy[p];
+#pragma unroll
+        for (int p = 0; p < kX; ++p) {
+            rows_u32x4 v[2];
+            decode16<E, MX>(from.x[p], from.sf[p], v);
+            *(lds_u32x4*)(lds + buf + x_to[p][0]) = v[0];
+            *(lds_u32x4*)(lds + buf + x_to[p][1]) = v[1];
+        }
+    };
+
+    int a_at[WM / 32], b_at[WN / 32];
+#pragma unroll
+    for (int i = 0; i < WM / 32; ++i)
+        a_at[i] = frag_at<BM>(wm + i * 32, lane);
+#pragma unroll
+    for (int j = 0; j < WN / 32; ++j)
+        b_at[j] = kStage * BM * 2 + frag_at<BN>(wn + j * 32, lane);
     v16f acc[WM / 32][WN / 32];
+    const auto multiply = [&](int buf, int r0, int r1) {
+#pragma unroll
+        for (int r = r0; r < r1; r += 16) {
+            Frag fa[WM / 32], fb[WN / 32];
+#pragma unroll
+            for (int i = 0; i < WM / 32; ++i)
+                fa[i] = read_frag<BM>(lds + buf + a_at[i], r);
+#pragma unroll
+            for (int j = 0; j < WN / 32; ++j)
+                fb[j] = read_frag<BN>(lds + buf + b_at[j], r);
+#pragma unroll
+            for (int i = 0; i < WM / 32; ++i)
+#pragma unroll
+                for (int j = 0; j < WN / 32; ++j)
+                    acc[i][j] = mfma(E{}, fa[i], fb[j], acc[i][j]);
+        }
+    };
+    // While stage t is multiplied, t + 1, loaded during t - 1, goes from registers to the
+    // other buffer, and t + 2 is loaded in its place.
+    Regs regs;
+    load(0, regs);
+    store(0, regs);
+    load(1, regs);
 #pragma unroll
     for (int i = 0; i < WM / 32; ++i)
 #pragma unroll
@@ -306,35 +363,18 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 acc[i][j][k] = 0.f;
-
-    if (stages > 0) {
-        load(0);
-        store(lds[0]);
-    }
     __syncthreads();
-    for (int t = 0; t < stages; ++t) {
-        if (t + 1 < stages)
-            load(t + 1);
-        char* const dt = lds[t & 1];
-        char* const xt = dt + kStage * BM * 2;
-#pragma unroll
-        for (int r = 0; r < kStage; r += 16) {
-            Frag fa[WM / 32], fb[WN / 32];
-#pragma unroll
-            for (int i = 0; i < WM / 32; ++i)
-                fa[i] = read_frag<BM>(dt, r, wm + i * 32, lane);
-#pragma unroll
-            for (int j = 0; j < WN / 32; ++j)
-                fb[j] = read_frag<BN>(xt, r, wn + j * 32, lane);
-#pragma unroll
-            for (int i = 0; i < WM / 32; ++i)
-#pragma unroll
-                for (int j = 0; j < WN / 32; ++j)
-                    acc[i][j] = mfma(E{}, fa[i], fb[j], acc[i][j]);
+    if (stages > 0) {
+        int from = 0;
+        for (int t = 1; t < stages; ++t) {
+            multiply(from, 0, 16);
+            store(kBytes - from, regs);  // (here, not after the last product: its latency lies under the rest)
+            load(t + 1, regs);
+            multiply(from, 16, kStage);
+            from = kBytes - from;
+            __syncthreads();
         }
-        if (t + 1 < stages)
-            store(lds[(t + 1) & 1]);
-        __syncthreads();
+        multiply(from, 0, kStage);
     }
 
     if (a.split == 1 && a.accumulate && rows == 0)
@@ -383,33 +423,60 @@ __global__ __launch_bounds__(256) void wgrad_join(WgradArgs a)
 
 namespace {
 
-int64_t tiles_of(int n, int k) { return (int64_t)((n + 127) / 128) * ((k + 127) / 128); }
+// The kernels: a tile's rows and columns, workgroups that run at a time, and in us a stage of
+// 64 rows with one workgroup on the card and with all of them, and a tile's start and results.
+struct Kind {
+    int bm, bn, slots;
+    float alone, busy, fixed;
+};
+constexpr Kind kKinds[] = {{128, 128, 512, 0.76f, 1.18f, 5.0f},
+                           {128, 256, 256, 0.92f, 1.13f, 5.5f},
+                           {256, 256, 256, 1.35f, 1.78f, 7.5f}};
 
 template <class E, bool MX>
 hipError_t launch(const WgradArgs& a, hipStream_t s)
 {
-#ifndef CFG
-#define CFG 128, 128, 64, 64, 32
-#endif
-    constexpr int cfg[] = {CFG};
-    constexpr int BM = cfg[0], BN = cfg[1], TH = cfg[0]/cfg[2]*cfg[1]/cfg[3]*64;
-    const int tm = (a.N + BM - 1) / BM, tn = (a.K + BN - 1) / BN;
-    const int64_t wgs = (int64_t)a.E * a.split * (((int64_t)tm * tn + 7) / 8 * 8);
+    const Kind& kind = kKinds[a.kind];
+    const int tm = (a.N + kind.bm - 1) / kind.bm, tn = (a.K + kind.bn - 1) / kind.bn;
+    const int64_t tiles = (int64_t)tm * tn;
+    const int64_t wgs = a.E == 1 ? (tiles * a.split + 7) / 8 * 8 : (int64_t)a.E * a.split * ((tiles + 7) / 8 * 8);
     if (wgs >= (INT64_C(1) << 31))
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((wgrad_tile<E, MX, CFG>), grid_of(wgs), dim3(TH), 0, s, a, tm, tn);
+    const auto kernel = a.kind == 0   ? wgrad_tile<E, MX, 128, 128, 64, 64, 64>
+                        : a.kind == 1 ? wgrad_tile<E, MX, 128, 256, 64, 64, 64>
+                                      : wgrad_tile<E, MX, 256, 256, 128, 64, 64>;
+    hipLaunchKernelGGL(kernel, grid_of(wgs), dim3(a.kind == 0 ? 256 : 512), 0, s, a, tm, tn);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int wgrad_split(int groups, int rows, int n, int k)
+void wgrad_choose(int groups, int rows, int n, int k, int& kind, int& split)
 {
-    const int64_t tiles = groups * tiles_of(n, k);
-    int split = 1;
-    while (split < kMostSplit && tiles * split < 256 && (int64_t)rows / groups >= (int64_t)split * 2 * 256)
-        split *= 2;
-    return split;
+    float least = 0;
+    kind = 0;
+    split = 1;
+    for (int i = 0; i < 3; ++i) {
+        const Kind& t = kKinds[i];
+        const int64_t tiles = (int64_t)groups * ((n + t.bm - 1) / t.bm) * ((k + t.bn - 1) / t.bn);
+        for (int s = 1; s <= kMostSplit; ++s) {
+            const int64_t per = ((int64_t)rows / groups + s - 1) / s;
+            if (s > 1 && (per < 4 * kShareRows || tiles * (s - 1) >= t.slots))
+                break;
+            const int64_t full = tiles * s / t.slots, left = tiles * s - full * t.slots;
+            const float stages = (float)((per + 63) / 64);
+            float us = (float)full * (stages * t.busy + t.fixed);
+            if (left > 0)
+                us += stages * (t.alone + (t.busy - t.alone) * (float)left / (float)t.slots) + t.fixed;
+            if (s > 1)  // the shares' sums written, read and added
+                us += 4.f + (float)groups * (float)n * (float)k * 4.f * (2 * s + 1) / 5e6f;
+            if (least == 0 || us < least) {
+                least = us;
+                kind = i;
+                split = s;
+            }
+        }
+    }
 }
 
 hipError_t launch_gemm_wgrad(const WgradArgs& a, hipStream_t s)

@@ -206,7 +206,9 @@ int check_wgrad(int32_t groups, int32_t rows, int32_t n, int32_t k)
 
 size_t wgrad_workspace(int32_t groups, int32_t rows, int32_t n, int32_t k)
 {
-    const int split = rows > 0 && n > 0 ? moe::wgrad_split(groups, rows, n, k) : 1;
+    int kind, split = 1;
+    if (rows > 0 && n > 0)
+        moe::wgrad_choose(groups, rows, n, k, kind, split);
     return split > 1 ? static_cast<size_t>(split) * groups * n * k * 4 : 0;
 }
 
@@ -728,7 +730,7 @@ int moe_gemm_wgrad(int32_t groups, int32_t rows, int32_t n, int32_t k, int32_t d
     a.accumulate = accumulate != 0;
     a.dw = static_cast<char*>(dw);
     a.partial = static_cast<float*>(workspace);
-    a.split = need > 0 ? moe::wgrad_split(groups, rows, n, k) : 1;
+    moe::wgrad_choose(groups, rows, n, k, a.kind, a.split);
     return launched(moe::launch_gemm_wgrad(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -113,7 +113,7 @@ struct WgradArgs {
     bool accumulate;
     char* dw;
     float* partial;            // [split, E, N, K], split > 1
-    int32_t split;             // workgroups that share a tile's rows
+    int32_t kind, split;       // the tile's kernel, and workgroups that share a tile's rows
 };
 
 hipError_t launch_gate(const GateArgs& a, hipStream_t s);
@@ -124,8 +124,8 @@ hipError_t launch_rms_norm_bwd(const NormArgs& a, hipStream_t s);
 int norm_partials(int rows, int width);
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
 hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t s);
-// The split of a call (host only).
-int wgrad_split(int groups, int rows, int n, int k);
+// The kernel and split of a call (host only).
+void wgrad_choose(int groups, int rows, int n, int k, int& kind, int& split);
 hipError_t launch_gemm_wgrad(const WgradArgs& a, hipStream_t s);
 hipError_t launch_permute(const RowsArgs& a, hipStream_t s);
 hipError_t launch_unpermute(const RowsArgs& a, hipStream_t s);  // also permute's gradient

@@ -140,6 +140,25 @@ def test_segments_without_counts_and_bad_lists():
         assert torch.equal(moe.moe_gemm_wgrad(*d, out=old.clone(), accumulate=True, **kw), old)
 
 
+def test_shares_of_experts_with_and_without_rows():
+    # rows of few experts split over workgroups, added to what is there: the experts' planes meet inside a wave
+    say("shares of experts")
+    R, n, k = 6000, 130, 96
+    dy, codes, sf, _ = make((R, 0, n, k, 1), torch.bfloat16, 1, 4)
+    d = (dy.cuda(), codes.cuda(), sf.cuda())
+    assert moe.moe_gemm_wgrad_workspace_bytes(3, R, n, k) > 3 * n * k * 4
+    for counts in ((0, R, 0), (R, 0, 0), (5, 0, R - 5), (0, 0, 0)):
+        off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32).cuda()
+        old = torch.randn(3, n, k, device="cuda")
+        fresh = moe.moe_gemm_wgrad(*d, offsets=off)
+        added = moe.moe_gemm_wgrad(*d, offsets=off, out=old.clone(), accumulate=True)
+        for e, c in enumerate(counts):
+            rows = slice(sum(counts[:e]), sum(counts[:e]) + c)
+            w, m, most = plain(dy[rows], x_values(codes[rows], sf[rows], torch.bfloat16), None, 0)
+            lu.within(fresh[e], w, bound_of(w, m, most, torch.float32))
+            assert torch.equal(added[e], old[e] + fresh[e] if c else old[e])
+
+
 def test_strides_and_odd_addresses():
     say("weight gradient strides")
     for n in (64, 71, 130):
