@@ -11,7 +11,10 @@
 // One wave per token, each lane a run of N adjacent experts in registers, so that the
 // lowest lane holding a maximum also holds the lowest id.  Values are compared as
 // integers in the order of the values (NaN on top, 0 for experts that cannot be
-// chosen), whose maximum over a wave is six instructions.
+// chosen), whose maximum over a wave is a handful of instructions.  c and the groups' sums
+// are formed in f32 first: where neighbours of the choice are further apart than f32
+// can be off (all but some of a thousand tokens of ordinary logits), the choice is that of
+// the formula; elsewhere the token's c are formed in 64 bits.
 #include "../../include/moe_ops.h"
 #include "ops_internal.h"
 #include "rows_device.h"
@@ -119,116 +122,99 @@ __device__ __forceinline__ void store_run(char* row, int e0, int n, const float*
     }
 }
 
-// m and the sum of exp(l - m) over the row (m NaN with a NaN in the row).
+// exp by the hardware's 2^x: off by 2 |x| + 2 roundings, zero below 2^-126.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
+// m, the terms exp(l - m) and their sum over the row (m passes NaN over, the sum does not).
 template <int N>
-__device__ __forceinline__ float softmax_sum(const float* l, float& m)
+__device__ __forceinline__ float softmax_sum(const float* l, float& m, float* e)
 {
-    uint32_t k = 0;
+    m = l[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        k = max(k, order32(l[i]));
-    m = from_order32(wave_max(k));
+    for (int i = 1; i < N; ++i)
+        m = fmaxf(m, l[i]);
+    m = from_order32(wave_max(order32(m)));
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        z += expf(l[i] - m);
+        z += e[i] = fast_exp(l[i] - m);
     return wave_sum(z);
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
 
-// The largest key of the wave: its lane (the lowest of equals); false if all keys are 0.
+// A lower bound of how far f32 values of c have to be apart for their order to be sure: each
+// is off by less than 64 roundings (softmax: 2 x e^-x of its own term, twice the mean
+// |x| of the sum's, below log E, 2 each of exp and quotient, 24 of the sum; the bias' sum one).
+__device__ __forceinline__ bool near(float above, float below, int terms)
+{
+    return !(above - below > 0x1p-17f * (float)terms * (1.f + fabsf(above)));
+}
+
+// The largest key of the wave: its lane (the lowest of equals); 0 if all keys are 0.
 template <bool WIDE>
-__device__ __forceinline__ bool wave_best(uint32_t hi, uint32_t lo, int& lane)
+__device__ __forceinline__ uint32_t wave_best(uint32_t hi, uint32_t lo, int& lane)
 {
     const uint32_t top = wave_max(hi);
-    if (top == 0)
-        return false;
     uint64_t who = __ballot(hi == top);
     if (WIDE && (who & (who - 1))) {
         const uint32_t low = wave_max(hi == top ? lo : 0u);
         who = __ballot(hi == top && lo == low);
     }
     lane = __builtin_ctzll(who);
-    return true;
+    return top;
 }
 
-}  // namespace
-
-// WIDE: the choice, or the groups' sums, need the scores in 64 bits.  LDS: E keys
-// of 8 bytes per wave with groups.
-template <class E, int N, bool WIDE>
-__global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_size, unsigned magic)
+// Takes the experts of other than the best groups out (their keys become 0).  `sums`: the
+// groups' sums are of values that may be off; true then if the last group in and the
+// first one out are too near.  WIDE: keys of 64 bits.
+template <int N, bool WIDE>
+__device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, unsigned magic, uint64_t* keys, int lane,
+                                            bool sums, uint32_t* hi, uint32_t* lo)
 {
-    extern __shared__ uint64_t group_keys[];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = (int64_t)workgroup() * kWaves + wave;
-    if (t >= a.T)
-        return;
-    int32_t* const idx = a.idx + t * a.K;
-    float* const w = a.w + t * a.K;
-    if (a.mask && !a.mask[t]) {
-        if (lane < a.K) {
-            idx[lane] = -1;
-            w[lane] = 0.f;
+    const int e0 = lane * N, lanes = group_size / N;
+    // groups of whole lanes, 1 to 16 of them: the best two by swaps inside the group
+    const bool whole = !WIDE && lanes * N == group_size && lanes <= 16 && (lanes & (lanes - 1)) == 0 && a.group_top <= 2;
+    uint32_t group_hi = 0, group_lo = 0;
+    if (whole) {
+        uint32_t one = hi[0], two = 0;
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            two = max(two, min(one, hi[i]));
+            one = max(one, hi[i]);
         }
-        return;
-    }
-    const char* const row = a.logits + t * a.ld;
-    const int e0 = lane * N;
-    float l[N];
-    load_run<E, N>(row, e0, a.E, l);
-
-    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-    float m = 0.f, z = 1.f;
-    if (softmax)
-        z = softmax_sum<N>(l, m);
-
-    // keys: the logits' order, or (WIDE) that of c in 64 bits
-    uint32_t hi[N], lo[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        hi[i] = l[i] == -INFINITY ? 0u : order32(l[i]);
-        lo[i] = 0;
-    }
-    if constexpr (WIDE) {
-        double c[N], zd = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            c[i] = exp(softmax ? (double)l[i] - (double)m : -(double)l[i]);
-        if (softmax) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                zd += c[i];
-            zd = wave_sum(zd);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const double s = softmax ? c[i] / zd : 1.0 / (1.0 + c[i]);
-            const float b = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
-            const bool on = l[i] != -INFINITY && b != -INFINITY;
-            const uint64_t k = on ? order64(s + (double)b) : 0;
-            hi[i] = (uint32_t)(k >> 32);
-            lo[i] = (uint32_t)k;
-        }
-    }
-
-    if (a.groups > 1) {
-        uint64_t* const keys = group_keys + wave * a.E;
+        const auto merge = [&](uint32_t b1, uint32_t b2) {
+            two = max(max(two, b2), min(one, b1));
+            one = max(one, b1);
+        };
+        if (lanes > 1)
+            merge(row_perm_u<0xB1>(one), row_perm_u<0xB1>(two));
+        if (lanes > 2)
+            merge(row_perm_u<0x4E>(one), row_perm_u<0x4E>(two));
+        if (lanes > 4)
+            merge(row_perm_u<0x141>(one), row_perm_u<0x141>(two));
+        if (lanes > 8)
+            merge(row_perm_u<0x140>(one), row_perm_u<0x140>(two));
+        group_hi = one;
+        if (a.group_top == 2 && two != 0)
+            group_hi = order32(from_order32(one) + from_order32(two));
+        // (one lane stands for the group)
+        if ((lane & (lanes - 1)) != 0)
+            group_hi = 0;
+    } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (e0 + i < a.E)
-                keys[e0 + i] = (uint64_t)hi[i] << 32 | lo[i];
+                keys[e0 + i] = (uint64_t)hi[i] << 32 | (WIDE ? lo[i] : 0u);
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         // lane g sums group g's best: each pass finds the largest key behind the
         // last one's (key descending, id ascending)
-        uint64_t group_key = 0;
         if (lane < a.groups) {
             const uint64_t* const of = keys + lane * group_size;
             uint64_t last = ~UINT64_C(0);
             int last_at = -1;
             double sum = 0;
+            float sum32 = 0.f;
             for (int p = 0; p < a.group_top; ++p) {
                 uint64_t best = 0;
                 int at = group_size;
@@ -247,58 +233,188 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
                 if (WIDE)
                     sum += from_order64(best);
                 else
-                    group_key = best;  // (group_top is 1)
+                    sum32 += from_order32((uint32_t)(best >> 32));
                 last = best;
                 last_at = at;
             }
-            if (WIDE && last_at >= 0)
-                group_key = order64(sum);
+            if (last_at >= 0) {
+                const uint64_t k = WIDE ? order64(sum) : a.group_top == 1 ? last : (uint64_t)order32(sum32) << 32;
+                group_hi = (uint32_t)(k >> 32);
+                group_lo = (uint32_t)k;
+            }
         }
-        uint64_t kept = 0;
-        for (int p = 0; p < a.top_groups; ++p) {
-            int g;
-            if (!wave_best<true>((uint32_t)(group_key >> 32), (uint32_t)group_key, g))
-                break;
-            kept |= UINT64_C(1) << g;
-            if (lane == g)
-                group_key = 0;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    }
+    const int shift = whole ? __builtin_ctz(lanes) : 0;
+    uint64_t kept = 0;
+    uint32_t last = 0;
+    bool close = false;
+    for (int p = 0; p <= a.top_groups; ++p) {
+        int from;
+        const uint32_t top = wave_best<WIDE>(group_hi, group_lo, from);
+        if (top == 0)
+            break;
+        if (p == a.top_groups) {
+            close = sums && near(from_order32(last), from_order32(top), a.group_top);
+            break;
         }
+        kept |= UINT64_C(1) << (from >> shift);
+        if (lane == from)
+            group_hi = group_lo = 0;
+        last = top;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const unsigned g = whole ? (unsigned)lane >> shift : (unsigned)(e0 + i) * magic >> 20;  // (e0 + i) / group_size
+        if (e0 + i >= a.E || !(kept >> (g & 63) & 1))
+            hi[i] = lo[i] = 0;
+    }
+    return close;
+}
+
+// The K largest keys, the j-th's expert in lane j.  `sums`: true if two that follow one
+// another, the last one in and the first one out among them, are too near.
+template <int N, bool WIDE>
+__device__ __forceinline__ bool pick(int K, int lane, bool sums, uint32_t* hi, uint32_t* lo, int& mine)
+{
+    bool close = false;
+    uint32_t last = 0;
+    mine = -1;
+    for (int j = 0; j < K + (sums ? 1 : 0); ++j) {
+        uint32_t best_hi = hi[0], best_lo = lo[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            if (WIDE)
+                best_lo = hi[i] > best_hi ? lo[i] : hi[i] == best_hi ? max(best_lo, lo[i]) : best_lo;
+            best_hi = max(best_hi, hi[i]);
+        }
+        int from;
+        const uint32_t top = wave_best<WIDE>(best_hi, best_lo, from);
+        if (top == 0)
+            break;
+        if (sums && j > 0)
+            close = close || near(from_order32(last), from_order32(top), 1);
+        last = top;
+        if (j == K)
+            break;
+        // of that lane's experts the first that has the key
+        const uint32_t low = WIDE ? lane_of(best_lo, from) : 0u;
+        int at = N;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+            if (lane_of(hi[i], from) == top && (!WIDE || lane_of(lo[i], from) == low))
+                at = i;
+        if (lane == j)
+            mine = from * N + at;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane == from && i == at)
+                hi[i] = lo[i] = 0;
+    }
+    return close;
+}
+
+}  // namespace
+
+// SUMS: the choice, or the groups', goes by sums that f32 rounds (a bias, or more than
+// one expert standing for a group).  LDS: E keys of 8 bytes per wave with groups.
+template <class E, int N, bool SUMS>
+__global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_size, unsigned magic)
+{
+    extern __shared__ uint64_t group_keys[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)workgroup() * kWaves + wave;
+    if (t >= a.T)
+        return;
+    int32_t* const idx = a.idx + t * a.K;
+    float* const w = a.w + t * a.K;
+    if (a.mask && !a.mask[t]) {
+        if (lane < a.K) {
+            idx[lane] = -1;
+            w[lane] = 0.f;
+        }
+        return;
+    }
+    uint64_t* const keys = group_keys + wave * a.E;
+    const char* const row = a.logits + t * a.ld;
+    const int e0 = lane * N;
+    float l[N], e[N], b[N];
+    load_run<E, N>(row, e0, a.E, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        b[i] = 0.f;
+    if (SUMS && a.bias) {
+        load_run<F32, N>(reinterpret_cast<const char*>(a.bias), e0, a.E, b);
+    }
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    float m = 0.f, z = 1.f;
+    if (softmax)
+        z = softmax_sum<N>(l, m, e);
+
+    uint32_t hi[N], lo[N];
+    bool close = false;
+    if constexpr (SUMS) {
+        // c in f32; what is not finite is left to 64 bits
+        const float rz = 1.f / z;
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const unsigned g = (unsigned)(e0 + i) * magic >> 20;  // (e0 + i) / group_size
-            if (e0 + i >= a.E || !(kept >> (g & 63) & 1))
-                hi[i] = lo[i] = 0;
-            else if (WIDE && !a.bias && hi[i] != 0) {  // the groups are chosen: back to the logits' order
+            const float s = softmax ? e[i] * rz : __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
+            const bool on = l[i] != -INFINITY && b[i] != -INFINITY;
+            const float c = s + b[i];
+            odd = odd || (on && !(fabsf(c) < INFINITY));
+            hi[i] = on ? order32(c) : 0u;
+            lo[i] = 0;
+        }
+        close = __ballot(odd) != 0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            hi[i] = l[i] == -INFINITY ? 0u : order32(l[i]);
+            lo[i] = 0;
+        }
+    }
+    // without a bias the experts' order is the logits', once the groups are chosen
+    const auto by_logits = [&] {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (hi[i] | lo[i]) {
                 hi[i] = order32(l[i]);
                 lo[i] = 0;
             }
-        }
-    }
-
-    // each lane its best expert; K times the wave's best, whose lane then looks for its next
-    int mine = -1;
-    uint32_t best_hi, best_lo;
-    int best_i;
-    const auto look = [&] {
-        best_hi = hi[0], best_lo = lo[0], best_i = 0;
-#pragma unroll
-        for (int i = 1; i < N; ++i)
-            if (hi[i] > best_hi || (WIDE && hi[i] == best_hi && lo[i] > best_lo))
-                best_hi = hi[i], best_lo = lo[i], best_i = i;
     };
-    look();
-    for (int j = 0; j < a.K; ++j) {
-        int from;
-        if (!wave_best<WIDE>(best_hi, best_lo, from))
-            break;
-        const int i_from = (int)lane_of((uint32_t)best_i, from);
-        if (lane == j)
-            mine = from * N + i_from;
+    int mine;
+    if (a.groups > 1 && !close)
+        close = keep_groups<N, false>(a, group_size, magic, keys, lane, SUMS, hi, lo);
+    if (SUMS && !a.bias)
+        by_logits();
+    if (!close)
+        close = pick<N, false>(a.K, lane, SUMS && a.bias, hi, lo, mine);
+    if (SUMS && close) {
+        double c[N], zd = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (lane == from && i == i_from)
-                hi[i] = lo[i] = 0;
-        look();
+            c[i] = exp(softmax ? (double)l[i] - (double)m : -(double)l[i]);
+        if (softmax) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                zd += c[i];
+            zd = wave_sum(zd);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double s = softmax ? c[i] / zd : 1.0 / (1.0 + c[i]);
+            const bool on = l[i] != -INFINITY && b[i] != -INFINITY;
+            const uint64_t k = on ? order64(s + (double)b[i]) : 0;
+            hi[i] = (uint32_t)(k >> 32);
+            lo[i] = (uint32_t)k;
+        }
+        if (a.groups > 1)
+            keep_groups<N, true>(a, group_size, magic, keys, lane, false, hi, lo);
+        if (!a.bias)
+            by_logits();
+        pick<N, true>(a.K, lane, false, hi, lo, mine);
     }
 
     // lane j the weight of slot j
@@ -336,16 +452,15 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
     if (slots != 0) {
         const char* const row = a.logits + t * a.ld;
         const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-        float l[N], m = 0.f, z = 1.f;
+        float l[N], e[N], m = 0.f, z = 1.f, v = 0.f, g = 0.f;
         load_run<E, N>(row, e0, a.E, l);
-        if (softmax)
-            z = softmax_sum<N>(l, m);
-        float p = 0.f, g = 0.f;
         if (mine >= 0) {
-            const float v = E::load(row + (int64_t)mine * E::SIZE);
-            p = softmax ? expf(v - m) / z : sigmoid(v);
+            v = E::load(row + (int64_t)mine * E::SIZE);
             g = a.scale * a.w[t * a.K + lane];
         }
+        if (softmax)
+            z = softmax_sum<N>(l, m, e);
+        const float p = mine < 0 ? 0.f : softmax ? expf(v - m) / z : sigmoid(v);
         float dp = g, q = 0.f;
         if (softmax || a.renorm)
             q = wave_sum(g * p);
@@ -370,13 +485,14 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
             for (int i = 0; i < N; ++i)
                 d[i] += at == i ? add : 0.f;
         }
+        const float rz = 1.f / z;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (softmax) {
-                d[i] *= expf(l[i] - m) / z;
+                d[i] *= e[i] * rz;
             } else {  // s (1 - s) without 1 - s, which loses the small ones
-                const float e = expf(-fabsf(l[i]));
-                d[i] *= e / ((1.f + e) * (1.f + e));
+                const float x = expf(-fabsf(l[i]));
+                d[i] *= x / ((1.f + x) * (1.f + x));
             }
         }
     }
@@ -399,8 +515,8 @@ hipError_t launch(const GateArgs& a, bool back, hipStream_t s)
     // e / size for e < 1024 and size <= 1024: the error, e (magic - 2^20 / size) / 2^20, stays below 1 / size
     const unsigned magic = ((1u << 20) + size - 1) / size;
     const size_t lds = a.groups > 1 ? (size_t)kWaves * a.E * 8 : 0;
-    const bool wide = a.bias || (a.groups > 1 && a.group_top > 1);
-    const auto kernel = wide ? gate_choose<E, N, true> : gate_choose<E, N, false>;
+    const bool sums = a.bias || (a.groups > 1 && a.group_top > 1);
+    const auto kernel = sums ? gate_choose<E, N, true> : gate_choose<E, N, false>;
     hipLaunchKernelGGL(kernel, grid, block, lds, s, a, size, magic);
     return hipGetLastError();
 }
