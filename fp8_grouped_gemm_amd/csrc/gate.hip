@@ -37,23 +37,51 @@ __device__ __forceinline__ float lane_of(float v, int lane)
     return __uint_as_float(lane_of(__float_as_uint(v), lane));
 }
 
+// v from another lane of the 16-lane row, in a form that the compiler folds into the
+// instruction that takes it.
+template <int CTRL>
+__device__ __forceinline__ uint32_t swap(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float swap(float v)
+{
+    return __uint_as_float(swap<CTRL>(__float_as_uint(v)));
+}
+
+constexpr int kNext = 0xB1, kPairs = 0x4E, kHalves = 0x141, kRow = 0x140;  // neighbours, pairs, mirrored halves and rows
+
 // The maximum over the wave, in every lane (a scalar).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-    v = max(v, row_perm_u<0xB1>(v));   // quad_perm [1,0,3,2]
-    v = max(v, row_perm_u<0x4E>(v));   // quad_perm [2,3,0,1]
-    v = max(v, row_perm_u<0x141>(v));  // row_half_mirror
-    v = max(v, row_perm_u<0x140>(v));  // row_mirror
+    v = max(v, swap<kNext>(v));
+    v = max(v, swap<kPairs>(v));
+    v = max(v, swap<kHalves>(v));
+    v = max(v, swap<kRow>(v));
     return max(max(lane_of(v, 0), lane_of(v, 16)), max(lane_of(v, 32), lane_of(v, 48)));
+}
+
+__device__ __forceinline__ float row_sum(float v)
+{
+    v += swap<kNext>(v);
+    v += swap<kPairs>(v);
+    v += swap<kHalves>(v);
+    v += swap<kRow>(v);
+    return v;
 }
 
 __device__ __forceinline__ float wave_sum(float v)
 {
-    v += row_perm<0xB1>(v);
-    v += row_perm<0x4E>(v);
-    v += row_perm<0x141>(v);
-    v += row_perm<0x140>(v);
+    v = row_sum(v);
     return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+// The sum over the first n lanes, the others' values being 0.
+__device__ __forceinline__ float slots_sum(float v, int n)
+{
+    return n <= 16 ? lane_of(row_sum(v), 0) : wave_sum(v);
 }
 
 __device__ __forceinline__ double wave_sum(double v)
@@ -141,7 +169,7 @@ __device__ __forceinline__ float softmax_sum(const float* l, float& m, float* e)
     return wave_sum(z);
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+__device__ __forceinline__ float sigmoid(float l) { return __builtin_amdgcn_rcpf(1.f + expf(-l)); }
 
 // A lower bound of how far f32 values of c have to be apart for their order to be sure: each
 // is off by less than 64 roundings (softmax: 2 x e^-x of its own term, twice the mean
@@ -188,19 +216,16 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
             one = max(one, b1);
         };
         if (lanes > 1)
-            merge(row_perm_u<0xB1>(one), row_perm_u<0xB1>(two));
+            merge(swap<kNext>(one), swap<kNext>(two));
         if (lanes > 2)
-            merge(row_perm_u<0x4E>(one), row_perm_u<0x4E>(two));
+            merge(swap<kPairs>(one), swap<kPairs>(two));
         if (lanes > 4)
-            merge(row_perm_u<0x141>(one), row_perm_u<0x141>(two));
+            merge(swap<kHalves>(one), swap<kHalves>(two));
         if (lanes > 8)
-            merge(row_perm_u<0x140>(one), row_perm_u<0x140>(two));
+            merge(swap<kRow>(one), swap<kRow>(two));
         group_hi = one;
         if (a.group_top == 2 && two != 0)
             group_hi = order32(from_order32(one) + from_order32(two));
-        // (one lane stands for the group)
-        if ((lane & (lanes - 1)) != 0)
-            group_hi = 0;
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -247,8 +272,31 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
     }
     const int shift = whole ? __builtin_ctz(lanes) : 0;
     uint64_t kept = 0;
-    uint32_t last = 0;
     bool close = false;
+    if (whole && a.groups <= 16) {
+        // a group's rank: how many are above it
+        const int own = lane >> shift;
+        int rank = own < a.groups ? 0 : 64;
+        for (int g = 0; g < a.groups; ++g) {
+            const uint32_t other = lane_of(group_hi, g << shift);
+            rank += other > group_hi || (other == group_hi && g < own);
+        }
+        if (sums) {
+            const uint64_t in = __ballot(rank == a.top_groups - 1), out = __ballot(rank == a.top_groups);
+            const uint32_t last = in ? lane_of(group_hi, __builtin_ctzll(in)) : 0u;
+            const uint32_t next = out ? lane_of(group_hi, __builtin_ctzll(out)) : 0u;
+            close = last != 0 && next != 0 && near(from_order32(last), from_order32(next), a.group_top);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (rank >= a.top_groups)
+                hi[i] = lo[i] = 0;
+        return close;
+    }
+    // (one lane stands for a group)
+    if (whole && (lane & (lanes - 1)) != 0)
+        group_hi = 0;
+    uint32_t last = 0;
     for (int p = 0; p <= a.top_groups; ++p) {
         int from;
         const uint32_t top = wave_best<WIDE>(group_hi, group_lo, from);
@@ -272,46 +320,56 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
     return close;
 }
 
-// The K largest keys, the j-th's expert in lane j.  `sums`: true if two that follow one
-// another, the last one in and the first one out among them, are too near.
+// The K largest keys, the j-th's expert in lane j (-1: there is none).  Each lane sorts its
+// own, equal ones by id, and shifts them down as they are taken.  `sums`: true if two
+// that follow one another, the last one in and the first one out among them, are too near.
 template <int N, bool WIDE>
 __device__ __forceinline__ bool pick(int K, int lane, bool sums, uint32_t* hi, uint32_t* lo, int& mine)
 {
-    bool close = false;
-    uint32_t last = 0;
-    mine = -1;
-    for (int j = 0; j < K + (sums ? 1 : 0); ++j) {
-        uint32_t best_hi = hi[0], best_lo = lo[0];
+    int id[N];
 #pragma unroll
-        for (int i = 1; i < N; ++i) {
-            if (WIDE)
-                best_lo = hi[i] > best_hi ? lo[i] : hi[i] == best_hi ? max(best_lo, lo[i]) : best_lo;
-            best_hi = max(best_hi, hi[i]);
+    for (int i = 0; i < N; ++i)
+        id[i] = i;
+#pragma unroll
+    for (int phase = 0; phase < N; ++phase)
+#pragma unroll
+        for (int i = phase & 1; i + 1 < N; i += 2) {
+            const bool above = hi[i + 1] > hi[i] || (WIDE && hi[i + 1] == hi[i] && lo[i + 1] > lo[i]);
+            const int one = id[i], two = id[i + 1];
+            id[i] = above ? two : one;
+            id[i + 1] = above ? one : two;
+            const uint32_t h1 = hi[i], h2 = hi[i + 1], l1 = lo[i], l2 = lo[i + 1];
+            hi[i] = above ? h2 : h1;
+            hi[i + 1] = above ? h1 : h2;
+            if (WIDE) {
+                lo[i] = above ? l2 : l1;
+                lo[i + 1] = above ? l1 : l2;
+            }
         }
+    mine = -1;
+    int top_of = 0, n = 0;  // lane j: the j-th key
+    uint32_t out = 0;       // the first one that is not taken
+    for (; n <= K; ++n) {
         int from;
-        const uint32_t top = wave_best<WIDE>(best_hi, best_lo, from);
-        if (top == 0)
+        out = wave_best<WIDE>(hi[0], lo[0], from);
+        if (out == 0 || n == K)
             break;
-        if (sums && j > 0)
-            close = close || near(from_order32(last), from_order32(top), 1);
-        last = top;
-        if (j == K)
-            break;
-        // of that lane's experts the first that has the key
-        const uint32_t low = WIDE ? lane_of(best_lo, from) : 0u;
-        int at = N;
+        const int taken = from * N + (int)lane_of((uint32_t)id[0], from);
+        mine = lane == n ? taken : mine;
+        top_of = lane == n ? (int)out : top_of;
+        if (lane == from) {
 #pragma unroll
-        for (int i = N - 1; i >= 0; --i)
-            if (lane_of(hi[i], from) == top && (!WIDE || lane_of(lo[i], from) == low))
-                at = i;
-        if (lane == j)
-            mine = from * N + at;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (lane == from && i == at)
-                hi[i] = lo[i] = 0;
+            for (int i = 0; i < N; ++i) {
+                hi[i] = i + 1 < N ? hi[i + 1] : 0u;
+                lo[i] = WIDE && i + 1 < N ? lo[i + 1] : 0u;
+                id[i] = i + 1 < N ? id[i + 1] : 0;
+            }
+        }
     }
-    return close;
+    if (!sums)
+        return false;
+    const uint32_t below = lane == n - 1 ? out : (uint32_t)__shfl_down(top_of, 1);
+    return __ballot(lane < n && below != 0 && near(from_order32((uint32_t)top_of), from_order32(below), 1)) != 0;
 }
 
 }  // namespace
@@ -356,18 +414,21 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
     bool close = false;
     if constexpr (SUMS) {
         // c in f32; what is not finite is left to 64 bits
-        const float rz = 1.f / z;
-        bool odd = false;
+        if (!softmax)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                e[i] = __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
+        const float rz = softmax ? __builtin_amdgcn_rcpf(z) : 1.f;
+        float odd = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float s = softmax ? e[i] * rz : __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
             const bool on = l[i] != -INFINITY && b[i] != -INFINITY;
-            const float c = s + b[i];
-            odd = odd || (on && !(fabsf(c) < INFINITY));
+            const float c = __builtin_fmaf(e[i], rz, b[i]);
+            odd += on ? c - c : 0.f;  // (0, or NaN of an infinity or a NaN)
             hi[i] = on ? order32(c) : 0u;
             lo[i] = 0;
         }
-        close = __ballot(odd) != 0;
+        close = __ballot(odd != 0.f) != 0;
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -384,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
                 lo[i] = 0;
             }
     };
-    int mine;
+    int mine = -1;
     if (a.groups > 1 && !close)
         close = keep_groups<N, false>(a, group_size, magic, keys, lane, SUMS, hi, lo);
     if (SUMS && !a.bias)
@@ -421,10 +482,10 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
     float s = 0.f;
     if (mine >= 0) {
         const float v = E::load(row + (int64_t)mine * E::SIZE);
-        s = softmax ? expf(v - m) / z : sigmoid(v);
+        s = softmax ? expf(v - m) * __builtin_amdgcn_rcpf(z) : sigmoid(v);
     }
     if (a.renorm)
-        s = s / (wave_sum(s) + kTiny);
+        s *= __builtin_amdgcn_rcpf(slots_sum(s, a.K) + kTiny);
     if (lane < a.K) {
         idx[lane] = mine;
         w[lane] = mine >= 0 ? a.scale * s : 0.f;
@@ -434,6 +495,7 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
 template <class E, int N>
 __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
 {
+    __shared__ __attribute__((aligned(16))) float slot_table[kWaves * 64 * N];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)workgroup() * kWaves + wave;
@@ -460,39 +522,61 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
         }
         if (softmax)
             z = softmax_sum<N>(l, m, e);
-        const float p = mine < 0 ? 0.f : softmax ? expf(v - m) / z : sigmoid(v);
+        const float rz = __builtin_amdgcn_rcpf(z);
+        const float p = mine < 0 ? 0.f : softmax ? expf(v - m) * rz : sigmoid(v);
         float dp = g, q = 0.f;
         if (softmax || a.renorm)
-            q = wave_sum(g * p);
+            q = slots_sum(g * p, a.K);
         if (a.renorm) {
-            const float total = wave_sum(p) + kTiny;
+            const float one = __builtin_amdgcn_rcpf(slots_sum(p, a.K) + kTiny);
             dp = kTiny * g;
             for (uint64_t left = slots; left; left &= left - 1) {
                 const int i = __builtin_ctzll(left);
                 dp = __builtin_fmaf(lane_of(p, i), g - lane_of(g, i), dp);
             }
-            dp = dp / total / total;
-            q = kTiny * q / total / total;
+            dp = dp * one * one;
+            q = kTiny * q * one * one;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)
             d[i] = softmax ? -q : 0.f;
-        for (uint64_t left = slots; left; left &= left - 1) {
-            const int j = __builtin_ctzll(left);
-            const int at = (int)lane_of((uint32_t)mine, j) - e0;
-            const float add = lane_of(dp, j);
+        // the slots' dp to their experts' lanes by way of LDS, unless an expert is named twice
+        float* const table = slot_table + wave * (64 * N);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            table[e0 + i] = 0.f;
+        const int named = lane + 1;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (mine >= 0)
+            table[mine] = __int_as_float(named);
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        const bool twice = mine >= 0 && __float_as_int(table[mine]) != named;
+        if (__ballot(twice) == 0) {
+            if (mine >= 0)
+                table[mine] = dp;
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                d[i] += at == i ? add : 0.f;
-        }
-        const float rz = 1.f / z;
+                d[i] += table[e0 + i];
+        } else {
+            for (uint64_t left = slots; left; left &= left - 1) {
+                const int j = __builtin_ctzll(left);
+                const int at = (int)lane_of((uint32_t)mine, j) - e0;
+                const float add = lane_of(dp, j);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (softmax) {
+                for (int i = 0; i < N; ++i)
+                    d[i] += at == i ? add : 0.f;
+            }
+        }
+        if (softmax) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
                 d[i] *= e[i] * rz;
-            } else {  // s (1 - s) without 1 - s, which loses the small ones
-                const float x = expf(-fabsf(l[i]));
-                d[i] *= x / ((1.f + x) * (1.f + x));
+        } else {  // s (1 - s) without 1 - s, which loses the small ones
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float x = expf(-fabsf(l[i])), r = __builtin_amdgcn_rcpf(1.f + x);
+                d[i] *= x * r * r;
             }
         }
     }
