@@ -31,6 +31,38 @@ __device__ __forceinline__ void store8(char* p, int n, const float* f)
     }
 }
 
+// Eight elements as they lie in memory, for loads that are used later.
+template <class T>
+struct Raw8 {
+    rows_u32x4 r[T::SIZE / 2];
+};
+
+template <class T>
+__device__ __forceinline__ Raw8<T> load_raw8(const char* p, int n)
+{
+    Raw8<T> v;
+    if (n >= 8) {
+#pragma unroll
+        for (int i = 0; i < T::SIZE / 2; ++i)
+            v.r[i] = load16(p + 16 * i);
+    } else {
+        float f[8];
+        load8<T>(p, n, f);
+#pragma unroll
+        for (int i = 0; i < T::SIZE / 2; ++i)
+            v.r[i] = T::pack(f + i * T::VEC);
+    }
+    return v;
+}
+
+template <class T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& v, float* f)
+{
+#pragma unroll
+    for (int i = 0; i < T::SIZE / 2; ++i)
+        T::unpack(v.r[i], f + i * T::VEC);
+}
+
 // Rounded to the type and back.
 template <class T>
 __device__ __forceinline__ void round8(float* f)

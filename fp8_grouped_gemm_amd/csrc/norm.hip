@@ -18,7 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxResident = 16384;
-constexpr int kPartials = 512;       // most partial rows of dw
+constexpr int kPartials = 256;       // most partial rows of dw
 constexpr int kColumnThreads = 256;
 
 __device__ __forceinline__ float wave_sum(float v)
@@ -29,8 +29,8 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// The sum over the TPR threads of a row; `red` is not written again before every
-// thread has passed another barrier.
+// The sum over the TPR threads of a row; `red` (one per wave) is not written again before
+// every thread has passed another barrier.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red)
 {
@@ -42,7 +42,7 @@ __device__ __forceinline__ float row_sum(float v, float* red)
         v = 0.f;
 #pragma unroll
         for (int i = 0; i < TPR / 64; ++i)
-            v += red[i];
+            v += red[threadIdx.x / TPR * (TPR / 64) + i];
     }
     return v;
 }
@@ -102,6 +102,11 @@ __device__ __forceinline__ float rstd_of(float sum, const NormArgs& a)
 }
 
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+constexpr int kGradThreads = 1024;
+
+// Threads along a row of a width that fits the registers.
+constexpr int row_threads(int width) { return width <= 1024 ? 64 : width <= 4096 ? 256 : width <= 8192 ? 512 : 1024; }
 
 }  // namespace
 
@@ -172,50 +177,48 @@ __global__ __launch_bounds__(1024) void norm_rows_wide(NormArgs a)
     }
 }
 
-// dx of a row whose sum of g xh is known, eight columns.
+// dx of a row whose mean of g xh is known, eight columns; d: what reaches z on its other way.
 template <class E>
 __device__ __forceinline__ void store_dx(const NormArgs& a, int64_t row, int col, int n, float rstd, float c,
-                                         const float* g, const float* xh)
+                                         const float* g, const float* xh, float* d)
 {
-    float d[8];
-    if (a.res) {
-        load8<E>(a.res + row * a.res_ld + (int64_t)col * E::SIZE, n, d);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            d[i] = 0.f;
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         d[i] = __builtin_fmaf(rstd, __builtin_fmaf(-xh[i], c, g[i]), d[i]);
     store8<E>(a.y + row * a.y_ld + (int64_t)col * E::SIZE, n, d);
 }
 
-// A row group (a workgroup, or a wave where TPR is 64) takes rows in steps of the
-// number of groups and keeps its columns' sums for dw.
+// kGradThreads / TPR rows at a time in each of `wgs` workgroups, whose columns' sums for dw
+// stay in registers over all its rows and meet in LDS at the end.
 template <class E, class W, int TPR, int CH, bool DX, bool DW>
-__global__ __launch_bounds__(threads_of(TPR)) void norm_grad(NormArgs a, int groups)
+__global__ __launch_bounds__(kGradThreads) void norm_grad(NormArgs a, int wgs)
 {
+    constexpr int ROWS = kGradThreads / TPR;
     __shared__ float red[2][16];
-    const int at = threadIdx.x % TPR;
-    const int group = blockIdx.x * (threads_of(TPR) / TPR) + threadIdx.x / TPR;
-    if (group >= groups)
-        return;
+    __shared__ __attribute__((aligned(16))) float part[DW && ROWS > 1 ? TPR * CH * 8 : 1];
+    const int at = threadIdx.x % TPR, group = threadIdx.x / TPR;
     float acc[CH][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc[c][i] = 0.f;
-    int turn = 0;
-    for (int64_t row = group; row < a.rows; row += groups, turn ^= 1) {
-        const float rstd = a.rstd[row];
+    const int turns = (a.rows + wgs * ROWS - 1) / (wgs * ROWS);
+    for (int turn = 0; turn < turns; ++turn) {
+        const int64_t row = ((int64_t)turn * wgs + blockIdx.x) * ROWS + group;
+        const int width = row < a.rows ? a.width : 0;
+        const float rstd = row < a.rows ? a.rstd[row] : 0.f;
         float g[CH][8], xh[CH][8], sum = 0.f;
+        Raw8<E> other[CH];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int col = (c * TPR + at) * 8, n = a.width - col;
-            load8<E>(a.x + row * a.x_ld + (int64_t)col * E::SIZE, n, g[c]);
-            load8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n, xh[c]);
+            const int col = (c * TPR + at) * 8, n = width - col;
+            const Raw8<E> dy = load_raw8<E>(a.x + row * a.x_ld + (int64_t)col * E::SIZE, n);
+            const Raw8<E> z = load_raw8<E>(a.z + row * a.z_ld + (int64_t)col * E::SIZE, n);
+            if (DX && a.res)
+                other[c] = load_raw8<E>(a.res + row * a.res_ld + (int64_t)col * E::SIZE, n);
+            unpack8<E>(dy, g[c]);
+            unpack8<E>(z, xh[c]);
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -235,20 +238,42 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_grad(NormArgs a, int gro
             }
         }
         if (DX) {
-            const float mean = row_sum<TPR>(sum, red[turn]) / (float)a.width;
+            const float mean = row_sum<TPR>(sum, red[turn & 1]) / (float)a.width;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int col = (c * TPR + at) * 8;
-                if (col < a.width)
-                    store_dx<E>(a, row, col, a.width - col, rstd, mean, g[c], xh[c]);
+                float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (a.res)
+                    unpack8<E>(other[c], d);
+                if (col < width)
+                    store_dx<E>(a, row, col, width - col, rstd, mean, g[c], xh[c], d);
             }
         }
     }
     if (DW) {
+        if constexpr (ROWS > 1) {
+            for (int r = 0; r < ROWS - 1; ++r) {
+                if (group == r)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float* const to = part + (c * TPR + at) * 8 + i;
+                            *to = r == 0 ? acc[c][i] : *to + acc[c][i];
+                        }
+                __syncthreads();
+            }
+            if (group != ROWS - 1)
+                return;
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int col = (c * TPR + at) * 8;
-            store8<F32>(reinterpret_cast<char*>(a.partial + (int64_t)group * a.width + col), a.width - col, acc[c]);
+            if constexpr (ROWS > 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[c][i] += part[col + i];
+            store8<F32>(reinterpret_cast<char*>(a.partial + (int64_t)blockIdx.x * a.width + col), a.width - col, acc[c]);
         }
     }
 }
@@ -286,7 +311,10 @@ __global__ __launch_bounds__(1024) void norm_dx_wide(NormArgs a)
     for (int col = threadIdx.x * 8; col < a.width; col += 1024 * 8) {
         float g[8], xh[8];
         load(col, g, xh);
-        store_dx<E>(a, row, col, a.width - col, rstd, mean, g, xh);
+        float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (a.res)
+            load8<E>(a.res + row * a.res_ld + (int64_t)col * E::SIZE, a.width - col, d);
+        store_dx<E>(a, row, col, a.width - col, rstd, mean, g, xh, d);
     }
 }
 
@@ -313,15 +341,16 @@ __global__ __launch_bounds__(kColumnThreads) void norm_dw_wide(NormArgs a, int g
     store8<F32>(reinterpret_cast<char*>(a.partial + (int64_t)p * a.width + col), n, acc);
 }
 
-// dw = sum of the partial rows: 64 columns a workgroup, 16 threads of four columns by 16
+// dw = sum of the partial rows: 32 columns a workgroup, 8 threads of four columns by 32
 // runs of rows, whose sums meet in LDS in ascending order.
 __global__ __launch_bounds__(256) void norm_dw_sum(const float* partial, int groups, int width, float* dw)
 {
-    __shared__ float part[16][64];
-    const int lane = threadIdx.x & 15, run = threadIdx.x >> 4;
-    const int col = blockIdx.x * 64 + lane * 4, n = width - col;
+    __shared__ float part[32][32];
+    const int lane = threadIdx.x & 7, run = threadIdx.x >> 3;
+    const int col = blockIdx.x * 32 + lane * 4, n = width - col;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p = run; p < groups; p += 16) {
+#pragma unroll 4
+    for (int p = run; p < groups; p += 32) {
         float v[4];
         load_vec<F32>(reinterpret_cast<const char*>(partial + (int64_t)p * width + col), n, v);
 #pragma unroll
@@ -332,18 +361,22 @@ __global__ __launch_bounds__(256) void norm_dw_sum(const float* partial, int gro
     for (int i = 0; i < 4; ++i)
         part[run][lane * 4 + i] = acc[i];
     __syncthreads();
-    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < width) {
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < width) {
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
+        for (int r = 0; r < 32; ++r)
             s += part[r][threadIdx.x];
-        dw[blockIdx.x * 64 + threadIdx.x] = s;
+        dw[blockIdx.x * 32 + threadIdx.x] = s;
     }
 }
 
 // ------------------------------------------------------------ launchers
 
-int norm_partials(int rows, int width) { return rows < kPartials ? rows : kPartials; }
+int norm_partials(int rows, int width)
+{
+    const int at_once = width <= kMaxResident ? kGradThreads / row_threads(width) : 1;
+    return min((rows + at_once - 1) / at_once, kPartials);
+}
 
 namespace {
 
@@ -356,10 +389,10 @@ hipError_t launch_rows(const NormArgs& a, bool back, hipStream_t s)
         hipLaunchKernelGGL((norm_rows<E, W, TPR, CH>), grid_of(((int64_t)a.rows + per - 1) / per), block, 0, s, a);
         return hipGetLastError();
     }
-    const int groups = norm_partials(a.rows, a.width);
+    const int wgs = norm_partials(a.rows, a.width);
     const auto kernel = a.y ? (a.dw ? norm_grad<E, W, TPR, CH, true, true> : norm_grad<E, W, TPR, CH, true, false>)
                             : norm_grad<E, W, TPR, CH, false, true>;
-    hipLaunchKernelGGL(kernel, dim3((groups + per - 1) / per), block, 0, s, a, groups);
+    hipLaunchKernelGGL(kernel, dim3(wgs), dim3(kGradThreads), 0, s, a, wgs);
     return hipGetLastError();
 }
 
@@ -430,7 +463,7 @@ hipError_t launch_rms_norm_bwd(const NormArgs& a, hipStream_t s)
             return e;
     }
     if (a.dw)
-        hipLaunchKernelGGL(norm_dw_sum, dim3((a.width + 63) / 64), dim3(256), 0, s, a.partial,
+        hipLaunchKernelGGL(norm_dw_sum, dim3((a.width + 31) / 32), dim3(256), 0, s, a.partial,
                            norm_partials(a.rows, a.width), a.width, a.dw);
     return hipGetLastError();
 }

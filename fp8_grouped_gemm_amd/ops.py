@@ -200,16 +200,34 @@ def _used(offsets, dev):
 _SF_BLOCK = {MOE_SF_F32_128: (128, torch.float32), MOE_SF_UE8M0_32: (32, torch.uint8)}
 
 
-def _new_codes(rows, cols, sf_format, codes, sf, device):
-    """The given (or new) code and scale tensors of 8-bit rows in a format."""
+def _out(t, name, dev, like, rows, width):
+    """A given output matrix of rows, checked, or a new one (which needs no check), of
+    like's type: the tensor, its address and its row stride."""
+    if t is None:
+        t = torch.empty((rows, width), dtype=like.dtype, device=like.device)
+        return t, t.data_ptr(), width
+    return t, t.data_ptr(), _rows(t, name, dev, like.dtype, rows, width)
+
+
+def _out_dense(t, name, dev, dtype, shape, device):
+    """A given densely packed output, checked, or a new one: the tensor and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    if t.requires_grad and torch.is_grad_enabled():
+        _lost(name)
+    return t, _dense(t, name, dev, dtype, shape)
+
+
+def _out_codes(codes, sf, name, dev, rows, cols, sf_format, device):
+    """The given (checked) or new code and scale tensors of 8-bit rows in a format, and
+    their addresses."""
     if sf_format not in _SF_BLOCK:
         raise ValueError(f"sf_format {sf_format}")
     block, dtype = _SF_BLOCK[sf_format]
-    if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.uint8, device=device)
-    if sf is None:
-        sf = torch.empty(rows, cols // block, dtype=dtype, device=device)
-    return codes, sf
+    codes, codes_at = _out_dense(codes, name + "codes", dev, torch.uint8, (rows, cols), device)
+    sf, sf_at = _out_dense(sf, name + "sf", dev, dtype, (rows, cols // block), device)
+    return codes, sf, codes_at, sf_at
 
 
 def _codes_at(codes, sf, name, dev, rows, cols, sf_format):
@@ -464,19 +482,13 @@ def moe_gate(logits, top_k, bias=None, mask=None, score=MOE_SCORE_SOFTMAX, group
     if mask is not None and mask.dtype is torch.bool:
         mask = mask.view(torch.uint8)
     given = tuple(t for t in (topk_idx, topk_w) if t is not None)
-    if topk_idx is None:
-        topk_idx = torch.empty(slots, dtype=torch.int32, device=logits.device)
-    if topk_w is None:
-        topk_w = torch.empty(slots, dtype=torch.float32, device=logits.device)
-    elif topk_w.requires_grad and torch.is_grad_enabled():
-        _lost("topk_w")
+    topk_idx, idx_at = _out_dense(topk_idx, "topk_idx", dev, torch.int32, slots, logits.device)
+    topk_w, w_at = _out_dense(topk_w, "topk_w", dev, torch.float32, slots, logits.device)
     _check(ops_lib().moe_gate(
         T, E, top_k, dt, logits.data_ptr(), _rows(logits, "logits", dev, logits.dtype, T, E),
         None if bias is None else _dense(bias, "bias", dev, torch.float32, (E,)),
         None if mask is None else _dense(mask, "mask", dev, torch.uint8, (T,)),
-        score, groups, top_groups, group_top, bool(renorm), scale,
-        _dense(topk_idx, "topk_idx", dev, torch.int32, slots),
-        _dense(topk_w, "topk_w", dev, torch.float32, slots), _raw_stream(dev)), "moe_gate")
+        score, groups, top_groups, group_top, bool(renorm), scale, idx_at, w_at, _raw_stream(dev)), "moe_gate")
     if given:
         _wrote(given)
     return topk_idx, topk_w
@@ -496,13 +508,11 @@ def moe_gate_bwd(logits, topk_idx, dw, score=MOE_SCORE_SOFTMAX, renorm=True, sca
     if dw.requires_grad and torch.is_grad_enabled():
         _lost("dw")
     given = out
-    if out is None:
-        out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    out, out_at, out_ld = _out(out, "out", dev, logits, T, E)
     _check(ops_lib().moe_gate_bwd(
         T, E, K, dt, logits.data_ptr(), _rows(logits, "logits", dev, logits.dtype, T, E),
         _dense(topk_idx, "topk_idx", dev, torch.int32, (T, K)), _dense(dw, "dw", dev, torch.float32, (T, K)),
-        score, bool(renorm), scale, out.data_ptr(), _rows(out, "out", dev, logits.dtype, T, E),
-        _raw_stream(dev)), "moe_gate_bwd")
+        score, bool(renorm), scale, out_at, out_ld, _raw_stream(dev)), "moe_gate_bwd")
     if given is not None:
         _wrote((given,))
     return out
@@ -520,34 +530,26 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, need_y=True, sf_format
                           sf)
     dev = x.get_device()
     dt, T, W = _matrix(x, "x", _DTYPES)
-    given = tuple(t for t, need in ((z, True), (rstd, True), (y, need_y), (codes, sf_format is not None),
-                                    (sf, sf_format is not None)) if need and t is not None)
+    eight = sf_format is not None
+    given = tuple(t for t in (z, rstd, y if need_y else None, *((codes, sf) if eight else ())) if t is not None)
     res_at = z_at = y_at = codes_at = sf_at = None
     res_ld = z_ld = y_ld = 0
     if residual is not None:
         res_at, res_ld = residual.data_ptr(), _rows(residual, "residual", dev, x.dtype, T, W)
-        if z is None:
-            z = torch.empty(T, W, dtype=x.dtype, device=x.device)
-        z_at, z_ld = z.data_ptr(), _rows(z, "z", dev, x.dtype, T, W)
+        z, z_at, z_ld = _out(z, "z", dev, x, T, W)
     elif z is not None:
         raise ValueError("z: without a residual it is x")
-    if rstd is None:
-        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    rstd, rstd_at = _out_dense(rstd, "rstd", dev, torch.float32, (T,), x.device)
     if need_y:
-        if y is None:
-            y = torch.empty(T, W, dtype=x.dtype, device=x.device)
-        y_at, y_ld = y.data_ptr(), _rows(y, "y", dev, x.dtype, T, W)
-    if sf_format is not None:
-        codes, sf = _new_codes(T, W, sf_format, codes, sf, x.device)
-        codes_at, sf_at = _codes_at(codes, sf, "", dev, T, W, sf_format)
+        y, y_at, y_ld = _out(y, "y", dev, x, T, W)
+    if eight:
+        codes, sf, codes_at, sf_at = _out_codes(codes, sf, "", dev, T, W, sf_format, x.device)
     w_at, w_dt = _norm_weight(weight, dev, x.dtype, W)
     _check(ops_lib().moe_rms_norm(
         T, W, dt, x.data_ptr(), _rows(x, "x", dev, x.dtype, T, W), res_at, res_ld, w_at, w_dt, eps, z_at, z_ld,
-        _dense(rstd, "rstd", dev, torch.float32, (T,)), y_at, y_ld, codes_at, sf_at, sf_format or 0,
-        _raw_stream(dev)), "moe_rms_norm")
+        rstd_at, y_at, y_ld, codes_at, sf_at, sf_format or 0, _raw_stream(dev)), "moe_rms_norm")
     if given:
         _wrote(given)
-    eight = sf_format is not None
     return z, rstd, (y if need_y else None), (codes if eight else None), (sf if eight else None)
 
 
@@ -580,15 +582,9 @@ def moe_rms_norm_bwd(dy, z, rstd, weight=None, dz=None, dx=None, dw=None, need_d
     if dz is not None:
         dz_at, dz_ld = dz.data_ptr(), _rows(dz, "dz", dev, dy.dtype, T, W)
     if need_dx:
-        if dx is None:
-            dx = torch.empty(T, W, dtype=dy.dtype, device=dy.device)
-        dx_at, dx_ld = dx.data_ptr(), _rows(dx, "dx", dev, dy.dtype, T, W)
+        dx, dx_at, dx_ld = _out(dx, "dx", dev, dy, T, W)
     if need_dw:
-        if dw is None:
-            dw = torch.empty(W, dtype=torch.float32, device=dy.device)
-        elif dw.requires_grad and torch.is_grad_enabled():
-            _lost("dw")
-        dw_at = _dense(dw, "dw", dev, torch.float32, (W,))
+        dw, dw_at = _out_dense(dw, "dw", dev, torch.float32, (W,), dy.device)
         if workspace is None:
             workspace = torch.empty(moe_rms_norm_bwd_workspace_bytes(T, W), dtype=torch.uint8, device=dy.device)
         ws_bytes = workspace.numel()
@@ -621,21 +617,18 @@ def moe_swiglu(gu, row_src=None, offsets=None, clamp=0.0, sf_format=None, need_h
     inner = W // 2
     given = tuple(t for t, need in ((h, need_h), (h_codes, need_h8), (h_sf, need_h8), (gu_codes, need_gu8),
                                     (gu_sf, need_gu8)) if need and t is not None)
-    h_at, h_ld, at = None, 0, [None] * 4
+    h_at = hc_at = hsf_at = gc_at = gsf_at = None
+    h_ld = 0
     if need_h:
-        if h is None:
-            h = torch.empty(R, inner, dtype=gu.dtype, device=gu.device)
-        h_at, h_ld = h.data_ptr(), _rows(h, "h", dev, gu.dtype, R, inner)
+        h, h_at, h_ld = _out(h, "h", dev, gu, R, inner)
     if need_h8:
-        h_codes, h_sf = _new_codes(R, inner, sf_format, h_codes, h_sf, gu.device)
-        at[:2] = _codes_at(h_codes, h_sf, "h_", dev, R, inner, sf_format)
+        h_codes, h_sf, hc_at, hsf_at = _out_codes(h_codes, h_sf, "h_", dev, R, inner, sf_format, gu.device)
     if need_gu8:
-        gu_codes, gu_sf = _new_codes(R, W, sf_format, gu_codes, gu_sf, gu.device)
-        at[2:] = _codes_at(gu_codes, gu_sf, "gu_", dev, R, W, sf_format)
+        gu_codes, gu_sf, gc_at, gsf_at = _out_codes(gu_codes, gu_sf, "gu_", dev, R, W, sf_format, gu.device)
     _check(ops_lib().moe_swiglu(
         R, inner, dt, gu.data_ptr(), _rows(gu, "gu", dev, gu.dtype, R, W), clamp,
         None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), _used(offsets, dev), h_at, h_ld,
-        *at, sf_format or 0, _raw_stream(dev)), "moe_swiglu")
+        hc_at, hsf_at, gc_at, gsf_at, sf_format or 0, _raw_stream(dev)), "moe_swiglu")
     if given:
         _wrote(given)
     return (h if need_h else None, *((h_codes, h_sf) if need_h8 else (None, None)),
@@ -660,12 +653,11 @@ def moe_swiglu_bwd(dh, gu=None, gu_codes=None, gu_sf=None, row_src=None, offsets
     else:
         fmt = _sf_format(gu_sf, "gu_sf")
         at = _codes_at(gu_codes, gu_sf, "gu_", dev, R, 2 * inner, fmt)
-    if out is None:
-        out = torch.empty(R, 2 * inner, dtype=dh.dtype, device=dh.device)
+    out, out_at, out_ld = _out(out, "out", dev, dh, R, 2 * inner)
     _check(ops_lib().moe_swiglu_bwd(
         R, inner, dt, dh.data_ptr(), _rows(dh, "dh", dev, dh.dtype, R, inner), gu_at, gu_ld, *at, fmt, clamp,
         None if row_src is None else _dense(row_src, "row_src", dev, torch.int32, R), _used(offsets, dev),
-        out.data_ptr(), _rows(out, "out", dev, dh.dtype, R, 2 * inner), _raw_stream(dev)), "moe_swiglu_bwd")
+        out_at, out_ld, _raw_stream(dev)), "moe_swiglu_bwd")
     if given is not None:
         _wrote((given,))
     return out
@@ -712,10 +704,7 @@ def moe_gemm_wgrad(dy, x, x_sf, offsets=None, counts=None, dtype=None, out=None,
         raise ValueError(f"dtype {dtype}")
     shape = (N, K) if offsets is None else (E, N, K)
     given, fmt = out, _sf_format(x_sf, "x_sf")
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dy.device)
-    elif out.requires_grad and torch.is_grad_enabled():
-        _lost("out")
+    out, out_at = _out_dense(out, "out", dev, dtype, shape, dy.device)
     x_at, sf_at = _codes_at(x, x_sf, "x_", dev, R, K, fmt)
     need = moe_gemm_wgrad_workspace_bytes(E, R, N, K)
     ws_at, ws_bytes = None, 0
@@ -728,7 +717,7 @@ def moe_gemm_wgrad(dy, x, x_sf, offsets=None, counts=None, dtype=None, out=None,
         E, R, N, K, dt, dy.data_ptr(), _rows(dy, "dy", dev, dy.dtype, R, N), x_at, sf_at, fmt,
         None if offsets is None else _dense(offsets, "offsets", dev, i32, E + 1),
         None if counts is None else _dense(counts, "counts", dev, i32, E), bool(accumulate),
-        _dense(out, "out", dev, dtype, shape), _DTYPES[dtype], ws_at, ws_bytes, _raw_stream(dev)), "moe_gemm_wgrad")
+        out_at, _DTYPES[dtype], ws_at, ws_bytes, _raw_stream(dev)), "moe_gemm_wgrad")
     if given is not None:
         _wrote((given,))
     return out

@@ -22,7 +22,7 @@ GATE_BWD = dict(T=4, E=64, K=4, dtype=BF16, p_logits=X, ld=0, p_idx=Y, p_dw=Z, s
 NORM = dict(rows=4, width=256, dtype=BF16, p_x=X, x_ld=0, p_res=Y, res_ld=0, p_weight=Z, w_dtype=F32, eps=1e-6,
             p_z=V, z_ld=0, p_rstd=V + 8192, p_y=W, y_ld=0, p_codes=U, p_sf=U + 4096, fmt=0, p_stream=0)
 NORM_BWD = dict(rows=4, width=256, dtype=BF16, p_dy=X, dy_ld=0, p_z=Y, z_ld=0, p_weight=Z, w_dtype=BF16, p_rstd=V,
-                p_dz=V + 4096, dz_ld=0, p_dx=W, dx_ld=0, p_dw=W + 8192, p_ws=U, ws_bytes=4 * 256 * 4, p_stream=0)
+                p_dz=V + 4096, dz_ld=0, p_dx=W, dx_ld=0, p_dw=W + 8192, p_ws=U, ws_bytes=256 * 4, p_stream=0)
 SWIGLU = dict(R=4, inner=128, dtype=BF16, p_gu=X, gu_ld=0, clamp=0.0, p_row_src=Y, p_used=Y + 4096, p_h=Z, h_ld=0,
               p_hc=V, p_hsf=V + 4096, p_gc=W, p_gsf=W + 4096, fmt=0, p_stream=0)
 SWIGLU_BWD = dict(R=4, inner=128, dtype=BF16, p_dh=X, dh_ld=0, p_gu=0, gu_ld=0, p_gc=Y, p_gsf=Y + 4096, fmt=0,
@@ -68,7 +68,7 @@ def call(name, base, **change):
         (dict(rows=-1), INV), (dict(width=0), INV), (dict(dtype=U8), INV), (dict(w_dtype=F16), INV),
         (dict(rows=1 << 28), SHAPE), (dict(width=1 << 24), SHAPE), (dict(p_dx=0, p_dw=0), INV),
         (dict(p_dy=0), INV), (dict(p_z=0), INV), (dict(p_rstd=0), INV), (dict(p_ws=0), INV),
-        (dict(ws_bytes=4 * 256 * 4 - 1), SMALL), (dict(p_ws=U + 8), INV), (dict(dy_ld=1), INV), (dict(z_ld=1), INV),
+        (dict(ws_bytes=256 * 4 - 1), SMALL), (dict(p_ws=U + 8), INV), (dict(dy_ld=1), INV), (dict(z_ld=1), INV),
         (dict(dz_ld=1), INV), (dict(dx_ld=1), INV), (dict(p_dx=X, dx_ld=300), INV), (dict(p_dx=Y), INV),
         (dict(p_dx=X + 2), INV), (dict(p_dw=Z), INV), (dict(p_dw=W), INV), (dict(p_ws=X), INV), (dict(p_ws=W), INV),
         (dict(p_dw=W + 8194), INV)]),
