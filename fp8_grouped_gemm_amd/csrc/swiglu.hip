@@ -5,9 +5,7 @@
 //
 // One thread takes eight columns of g and the same of u, and writes what the call asks
 // for: h, h in 8 bits, and gate and up in 8 bits, which the gradient reads in place of
-// the input.  Rows that hold no slot are passed over.  With e = exp(-|g|) and
-// r = 1 / (1 + e), sg and 1 - sg are r and e r (g < 0: the other way round): neither
-// overflows nor cancels.
+// the input.  Rows that hold no slot are passed over.
 #include "../../include/moe_ops.h"
 #include "fp8_rows.h"
 #include "ops_internal.h"
@@ -38,9 +36,15 @@ __device__ __forceinline__ bool place(const SwigluArgs& a, int tpr, int pieces, 
     return row < used && col < a.inner && (!a.row_src || a.row_src[row] >= 0);
 }
 
+// sg = 1 / (1 + exp(-g)) and 1 - sg of an element of type E.  With e = exp(-|g|) and
+// r = 1 / (1 + e) they are r and e r (g < 0: the other way round): neither overflows
+// nor cancels.  16-bit types take e from the hardware's 2^x: off by |g| + 2 roundings of f32 at
+// most, of which 2^15 make half a step of theirs, and zero below 2^-126.
+template <class E>
 __device__ __forceinline__ void sigmoid(float g, float& sg, float& rest)
 {
-    const float e = expf(-fabsf(g)), r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
+    const float e = E::SIZE == 4 ? expf(-fabsf(g)) : __builtin_amdgcn_exp2f(-1.44269504088896341f * fabsf(g));
+    const float r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
     sg = g < 0.f ? er : r;
     rest = g < 0.f ? r : er;
 }
@@ -89,7 +93,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_rows(SwigluArgs a, int tpr, i
             u[i] = clamped(u[i], a.clamp);
         }
         float sg, rest;
-        sigmoid(g[i], sg, rest);
+        sigmoid<E>(g[i], sg, rest);
         h[i] = g[i] * sg * u[i];
     }
     if (a.h)
@@ -124,8 +128,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad(SwigluArgs a, int tpr, i
         const int64_t cols = 2 * (int64_t)a.inner, row_bytes = MX ? cols / 32 : cols / 128 * 4;
         const uint8_t* const codes = a.gu_codes + row * cols + col;
         const char* const sf = static_cast<const char*>(a.gu_sf) + row * row_bytes;
-        decode8(*reinterpret_cast<const uint2*>(codes), read_scale<MX>(sf, col), g);
-        decode8(*reinterpret_cast<const uint2*>(codes + a.inner), read_scale<MX>(sf, a.inner + col), u);
+        decode8<MX>(*reinterpret_cast<const uint2*>(codes), read_scale<MX>(sf, col), g);
+        decode8<MX>(*reinterpret_cast<const uint2*>(codes + a.inner), read_scale<MX>(sf, a.inner + col), u);
     }
     float dg[8], du[8];
 #pragma unroll
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad(SwigluArgs a, int tpr, i
         const bool cu = a.clamp > 0.f && (u[i] > a.clamp || u[i] < -a.clamp);
         const float gc = cg ? clamped(g[i], a.clamp) : g[i], uc = cu ? clamped(u[i], a.clamp) : u[i];
         float sg, rest;
-        sigmoid(gc, sg, rest);
+        sigmoid<E>(gc, sg, rest);
         dg[i] = cg ? 0.f : dh[i] * uc * (sg * __builtin_fmaf(gc, rest, 1.f));
         du[i] = cu ? 0.f : dh[i] * (gc * sg);
     }
