@@ -57,7 +57,7 @@ def read(codes, sf):
 def quantised(v, fmt):
     """(codes, sf) of float32 rows by moe_quantize_act's rule: float32 quotients, rounded to nearest even."""
     v = v.detach().float().cpu()
-    blk = v.view(v.shape[0], -1, BLOCK[fmt])
+    blk = v.view(v.shape[0], v.shape[1] // BLOCK[fmt], BLOCK[fmt])
     s = blk.abs().amax(-1).clamp(min=1e-10) / 448.0
     if fmt == 1:
         m, e = torch.frexp(s)
@@ -78,7 +78,7 @@ def same_codes(codes, sf, v, fmt):
 def near_codes(codes, sf, want, rel, fmt):
     """codes and sf stand for float64 rows `want` whose float32 form may be off by `rel` of each value."""
     s = scales(sf)
-    amax = np.maximum(abs(want).reshape(want.shape[0], -1, BLOCK[fmt]).max(-1), float(np.float32(1e-10))) / 448
+    amax = np.maximum(abs(want).reshape(want.shape[0], want.shape[1] // BLOCK[fmt], BLOCK[fmt]).max(-1), float(np.float32(1e-10))) / 448
     if fmt == 1:                                              # a power of two: the least that covers it
         assert np.all(s >= amax * (1 - rel - 2 * U32)) and np.all(s < 2 * amax * (1 + rel + 2 * U32))
     else:
