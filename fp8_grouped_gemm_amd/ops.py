@@ -83,13 +83,17 @@ def ops_lib():
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
+# The current device's number without torch.cuda's check that it is initialised
+# (a tensor on a GPU shows that it is).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _here(t, stream):
     """Whether a call with tensor t and this stream argument runs on the
     current device and its current stream."""
     if not t.is_cuda:
         raise ValueError(f"tensors are on {t.device}, expected a GPU")
-    return stream is None and t.get_device() == torch.cuda.current_device()
+    return stream is None and t.get_device() == _current_device()
 
 
 def _elsewhere(fn, t, stream, *args, **kw):
@@ -204,7 +208,8 @@ def _out(t, name, dev, like, rows, width):
     """A given output matrix of rows, checked, or a new one (which needs no check), of
     like's type: the tensor, its address and its row stride."""
     if t is None:
-        t = torch.empty((rows, width), dtype=like.dtype, device=like.device)
+        t = (torch.empty_like(like) if like.shape == (rows, width) and like.is_contiguous() else
+             torch.empty((rows, width), dtype=like.dtype, device=like.device))
         return t, t.data_ptr(), width
     return t, t.data_ptr(), _rows(t, name, dev, like.dtype, rows, width)
 
