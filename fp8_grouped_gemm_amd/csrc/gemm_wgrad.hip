@@ -374,7 +374,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
             from = kBytes - from;
             __syncthreads();
         }
-        multiply(from, 0, kStage);
+        const int left = rows - (stages - 1) * kStage;  // (of the last stage only the steps that hold rows)
+#pragma unroll
+        for (int r = 0; r < kStage; r += 16)
+            if (r < left)
+                multiply(from, r, r + 16);
     }
 
     if (a.split == 1 && a.accumulate && rows == 0)
