@@ -235,9 +235,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
     rows = __builtin_amdgcn_readfirstlane(rows);
     const int stages = (rows + kStage - 1) / kStage;
     const int sf_row = MX ? a.K / 32 : a.K / 128 * 4;
-    const char* const dy = a.dy + first * a.dy_ld;
-    const uint8_t* const x = a.x + first * a.K;
-    const char* const sf = a.x_sf + first * sf_row;
+    // what is loaded next, and the bytes that are left of the share there
+    const char* dy = a.dy + first * a.dy_ld;
+    const char* x = reinterpret_cast<const char*>(a.x) + first * a.K;
+    const char* sf = a.x_sf + first * sf_row;
+    int64_t dy_left = rows > 0 ? (rows - 1) * a.dy_ld + a.N * 2 : 0, x_left = (int64_t)rows * a.K,
+            sf_left = (int64_t)rows * sf_row;
+    int rows_left = rows;
 
     // The thread's pieces of a stage: offsets from its first row, kOut for columns past the
     // matrix.  A buffer ends with the share's last row, so that rows past it (and kOut) read as
@@ -258,28 +262,21 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
         sf_at[p] = c < a.K ? r * (unsigned)sf_row + (MX ? c / 32 : c / 128 * 4) : kOut;
     }
     const bool cut_edge = a.N % 8 != 0 && m0 + BM > a.N;
-    const auto bytes_left = [&](int r0, int64_t ld, int64_t width) {
-        const int64_t n = (rows - r0 - 1) * ld + width;
-        return r0 < rows ? (unsigned)min(n, INT64_C(0x7FFFFFFF)) : 0u;
-    };
+    const auto bytes = [](int64_t left) { return (unsigned)min(max(left, INT64_C(0)), INT64_C(0x7FFFFFFF)); };
     struct Regs {
         rows_u32x4 dy[kDy], x[kX];
         uint32_t sf[kX];
     };
-    const auto load = [&](int stage, Regs& to) {
-        const int r0 = stage * kStage;
-        const auto db = buffer(dy + r0 * a.dy_ld, bytes_left(r0, a.dy_ld, a.N * 2));
-        const auto xb = buffer(x + (int64_t)r0 * a.K, bytes_left(r0, a.K, a.K));
-        const auto sb = buffer(sf + (int64_t)r0 * sf_row, bytes_left(r0, sf_row, sf_row));
+    const auto load = [&](Regs& to) {  // the next stage (zeros past the last)
+        const auto db = buffer(dy, bytes(dy_left)), xb = buffer(x, bytes(x_left)), sb = buffer(sf, bytes(sf_left));
         if (cut_edge && ragged) {
 #pragma unroll
             for (int p = 0; p < kDy; ++p) {
-                const int r = r0 + (p * kThreads + (int)threadIdx.x) / (BM / 8);
+                const int r = (p * kThreads + (int)threadIdx.x) / (BM / 8);
                 uint16_t v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[i] = i < ragged && r < rows
-                               ? reinterpret_cast<const uint16_t*>(dy + r0 * a.dy_ld + d_at[p])[i] : 0;
+                    v[i] = i < ragged && r < rows_left ? reinterpret_cast<const uint16_t*>(dy + d_at[p])[i] : 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     to.dy[p][i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
@@ -297,6 +294,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
             else
                 to.sf[p] = __builtin_amdgcn_raw_buffer_load_b32(sb, sf_at[p], 0, 0);
         }
+        dy += kStage * a.dy_ld;
+        x += (int64_t)kStage * a.K;
+        sf += (int64_t)kStage * sf_row;
+        dy_left -= kStage * a.dy_ld;
+        x_left -= (int64_t)kStage * a.K;
+        sf_left -= (int64_t)kStage * sf_row;
+        rows_left -= kStage;
     };
 
     int d_to[kDy], x_to[kX][2];
@@ -353,9 +357,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
     // While stage t is multiplied, t + 1, loaded during t - 1, goes from registers to the
     // other buffer, and t + 2 is loaded in its place.
     Regs regs;
-    load(0, regs);
+    load(regs);
     store(0, regs);
-    load(1, regs);
+    load(regs);
 #pragma unroll
     for (int i = 0; i < WM / 32; ++i)
 #pragma unroll
@@ -369,7 +373,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
         for (int t = 1; t < stages; ++t) {
             multiply(from, 0, 16);
             store(kBytes - from, regs);  // (here, not after the last product: its latency lies under the rest)
-            load(t + 1, regs);
+            load(regs);
             multiply(from, 16, kStage);
             from = kBytes - from;
             __syncthreads();
