@@ -33,7 +33,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) rows_u32x4 lds_u32x4;
 
 constexpr int kMostSplit = 16;
-constexpr int kStrip = 8;
+constexpr int kStrip = 4;
 constexpr int kShareRows = 64;  // shares are whole multiples of it
 
 struct Frag {
@@ -210,8 +210,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
 
     // Workgroups go to the 8 dies in turn.  Of every unit's (a share of an expert's) tiles, counted
     // down strips of kStrip rows, a die takes a run: a compact block, whose rows and
-    // columns its L2 holds; the die that gets the last, shorter one changes from unit to
-    // unit.  Shares of one expert are equally long, so that the dies take runs of them all.
+    // columns its L2 holds (32 experts of 384 rows, 4096 x 4096: 568 us with strips of 4
+    // tiles, 584 of 8, 596 of 16); the die that gets the last, shorter run changes from unit
+    // to unit.  Shares of one expert are equally long, so that the dies take runs of them all.
     const unsigned tiles = tiles_m * tiles_n, die = workgroup() & 7, turn = workgroup() >> 3;
     unsigned unit, tile;
     if (a.E == 1) {
