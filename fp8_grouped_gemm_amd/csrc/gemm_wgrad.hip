@@ -92,6 +92,17 @@ __device__ __forceinline__ Frag read_frag(lds_char* at, int r0)
     return f;
 }
 
+// code * scale in f32.  (A product that goes to f16 would be rounded by the instruction that
+// converts it, once instead of twice: both types take the f32 value, as the header says.)
+template <class E>
+__device__ __forceinline__ float product(float code, float scale)
+{
+    float p = code * scale;
+    if constexpr (__is_same(E, F16))
+        asm("" : "+v"(p));
+    return p;
+}
+
 // 16 codes times their scale, rounded to E: the eight of even and the eight of odd columns.
 // A power of two in one instruction (equal to the product's rounding for every code and
 // scale code, 0 and 0xFF among them; f16 keeps the sign of -0).
@@ -112,8 +123,8 @@ __device__ __forceinline__ void decode16(rows_u32x4 q, uint32_t sf, rows_u32x4* 
                 typedef float f2 __attribute__((ext_vector_type(2)));
                 const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
                 const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
-                out[h][2 * i] = E::pack2(a[0] * scale, a[1] * scale);
-                out[h][2 * i + 1] = E::pack2(b[0] * scale, b[1] * scale);
+                out[h][2 * i] = E::pack2(product<E>(a[0], scale), product<E>(a[1], scale));
+                out[h][2 * i + 1] = E::pack2(product<E>(b[0], scale), product<E>(b[1], scale));
             }
         }
 }

@@ -299,8 +299,8 @@ int moe_swiglu_bwd(int32_t pool_rows, int32_t inner, int32_t dtype, const void* 
  * Weight gradients from rows kept in 8 bits:
  *   dw[e, i, k] = sum over the rows r of expert e of dy[r, i] * x[r, k]
  *   dy     [rows, n] bf16 or f16 (dtype), row stride dy_ld, here at most 2^24
- *   x      uint8 [rows, k] e4m3, x_sf by sf_format: x[r, k] = code * scale, rounded to dy's
- *          type (exact in bf16 with UE8M0 scales above its subnormals)
+ *   x      uint8 [rows, k] e4m3, x_sf by sf_format: x[r, k] = the f32 product code * scale,
+ *          rounded to dy's type (exact in bf16 with UE8M0 scales above its subnormals)
  *   dw     [groups, n, k] bf16, f16 or f32 (dw_dtype), densely packed, rounded once from f32
  * Segments as in moe_gemm_mxfp4: offsets null: dense, groups 1, every row; else
  * expert e's rows are offsets[e] .. offsets[e] + counts[e] - 1 (counts null: up to

@@ -205,6 +205,22 @@ def test_rows_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+def test_widest_rows():
+    T, W = 2, (1 << 24) - 1
+    say(f"norm of {T} x {W}")
+    z, dy, w = make((T, W), torch.bfloat16, 3)
+    _, rstd, y, _, _ = moe.moe_rms_norm(z.cuda(), w.cuda(), eps=EPS)
+    want = lu.norm(lu.f64(z), 1.0, EPS)[0]
+    lu.within(rstd, want, lu.norm_steps(W) * lu.U32 * want)
+    check_y(y, lu.f64(z), lu.f64(w), torch.bfloat16)
+    r = torch.from_numpy(want).float()
+    dx, dw = moe.moe_rms_norm_bwd(dy.cuda(), z.cuda(), r.cuda(), w.cuda())
+    wx, mx, ww, mw = lu.norm_grads(lu.f64(dy), lu.f64(z), lu.f64(r), lu.f64(w), 0.0)
+    # as for the narrower rows: a thread's run, the trees, five products and sums; for dw two products and the rows' sum
+    lu.within(dx, wx, lu.rounded_bound(wx, (W / 1024 + 8 + 22 + 6) * lu.U32 * mx, torch.bfloat16))
+    lu.within(dw, ww, 4 * lu.U32 * mw + 2.0 ** -140)
+
+
 def test_binding_refusals():
     x, w, r = torch.randn(4, 64, device="cuda"), torch.randn(64, device="cuda"), torch.ones(4, device="cuda")
     leaf = x.clone().requires_grad_()

@@ -215,6 +215,11 @@ def test_pool_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+def test_widest_rows():
+    test_activation_against_the_plain_form((3, (1 << 23) - 128), "bf16")
+    test_gradient_against_the_formula((1, (1 << 23) - 1), "f16")
+
+
 def test_binding_refusals():
     gu, dh = torch.randn(4, 256, device="cuda"), torch.randn(4, 128, device="cuda")
     codes, sf = torch.zeros(4, 256, dtype=torch.uint8, device="cuda"), torch.zeros(4, 8, dtype=torch.uint8, device="cuda")

@@ -226,6 +226,57 @@ def test_rows_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+# rows, experts (0: dense), n, k, alignment, shares: sizes that the larger tiles take, whole and in shares of the rows
+LARGER = [(5805, 8, 399, 2048, 1, False), (4686, 0, 391, 2304, 1, True), (300, 8, 519, 1664, 1, False), (5679, 0, 1037, 2432, 1, True)]
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", 1), ("f16", 0)], ids=["bf16-ue8m0", "f16-f32"])
+@pytest.mark.parametrize("shape", LARGER, ids=str)
+def test_larger_products_against_the_plain_form(shape, dtype, fmt):
+    say(f"weight gradient {shape} {dtype} {fmt}")
+    dt, (rows, E, n, k, _, shares) = DT[dtype], shape
+    dy, codes, sf, lists = make(shape[:5], dt, fmt, 5)
+    assert (moe.moe_gemm_wgrad_workspace_bytes(max(1, E), len(dy), n, k) > 0) == shares
+    want, mag, most = plain(dy, x_values(codes, sf, dt), lists, E)
+    d = (dy.cuda(), codes.cuda(), sf.cuda())
+    got = moe.moe_gemm_wgrad(*d, **seg(lists))
+    lu.within(got, want, bound_of(want, mag, most, torch.float32))
+    assert torch.equal(moe.moe_gemm_wgrad(*d, dtype=torch.bfloat16, **seg(lists)), got.bfloat16())
+    old = torch.randn(got.shape, device="cuda")
+    none = torch.zeros(got.shape, dtype=torch.bool)
+    if E:
+        none[lists["counts"] == 0] = True
+    assert torch.equal(moe.moe_gemm_wgrad(*d, out=old.clone(), accumulate=True, **seg(lists)),
+                       torch.where(none.cuda(), old, old + got))
+    old = old.half()
+    assert torch.equal(moe.moe_gemm_wgrad(*d, out=old.clone(), accumulate=True, **seg(lists)),
+                       torch.where(none.cuda(), old, (old.float() + got).half()))
+
+
+def test_widest_stride():
+    # 130 rows 2^24 elements apart: stages that span all but 2^31 bytes
+    say("weight gradient of rows 32 MB apart")
+    for n in (40, 37):
+        dy, codes, sf, _ = make((130, 0, n, 64, 1), torch.bfloat16, 1, 6)
+        far = torch.empty(129 * (1 << 24) + n, dtype=torch.bfloat16, device="cuda").as_strided((130, n), (1 << 24, 1))
+        far.copy_(dy)
+        assert torch.equal(moe.moe_gemm_wgrad(far, codes.cuda(), sf.cuda()), moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda()))
+    del far
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n,k", [((1 << 20) - 1, 32), (3, 1 << 20)])
+def test_widest_matrices(n, k):
+    say(f"weight gradient {n} x {k}")
+    g = torch.Generator().manual_seed(7)
+    dy = torch.randint(-8, 9, (2, n), generator=g).bfloat16().cuda()
+    codes = torch.randint(0x30, 0x48, (2, k), generator=g).to(torch.uint8)  # 0.5 to 3.75 in sixteenths
+    sf = torch.full((2, k // 32), 127, dtype=torch.uint8, device="cuda")
+    xv = torch.from_numpy(lu.E4M3).float().cuda()[codes.cuda().long()]
+    got = moe.moe_gemm_wgrad(dy, codes.cuda(), sf)
+    assert torch.equal(got, dy[0].float()[:, None] * xv[0] + dy[1].float()[:, None] * xv[1])  # (whole sixteenths: exact)
+
+
 def test_workspace_and_refusals():
     say("weight gradient: refusals")
     dy, codes, sf, _ = (t.cuda() if isinstance(t, torch.Tensor) else t for t in make((3000, 0, 50, 128, 1), torch.bfloat16, 1))
