@@ -64,6 +64,25 @@ def test_choice_against_the_plain_form(shape, dtype):
                 check(l, got, K, b, m, sigmoid, groups, top_groups, group_top, renorm, scale)
 
 
+@pytest.mark.parametrize("run", [1, 2, 4, 6, 8, 16])
+def test_groups_of_whole_lanes(run):
+    # groups of 1 to 64 lanes' experts, few and many of them
+    for lanes in (1, 2, 4, 8, 16, 32):
+        groups, E = 64 // lanes, 64 * run
+        say(f"gate {E} experts in {groups} groups")
+        l, bias, mask, _ = draw((9, E), torch.float32, lanes)
+        for group_top in (1, 2):
+            top_groups = max(1, groups // 3)
+            K = min(5, lanes * run * top_groups)
+            if group_top > lanes * run:
+                continue
+            for sigmoid, b in ((False, bias), (True, bias), (True, None)):
+                got = moe.moe_gate(l.cuda(), K, bias=None if b is None else b.cuda(),
+                                   score=moe.MOE_SCORE_SIGMOID if sigmoid else moe.MOE_SCORE_SOFTMAX,
+                                   groups=groups, top_groups=top_groups, group_top=group_top)
+                check(l, got, K, b, None, sigmoid, groups, top_groups, group_top, True, 1.0)
+
+
 def test_ties_go_to_the_lower_id():
     say("ties")
     T, E = 40, 320
