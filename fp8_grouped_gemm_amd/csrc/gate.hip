@@ -19,6 +19,8 @@
 #include "ops_internal.h"
 #include "rows_device.h"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -49,6 +51,17 @@ template <int CTRL>
 __device__ __forceinline__ float swap(float v)
 {
     return __uint_as_float(swap<CTRL>(__float_as_uint(v)));
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint64_t swap(uint64_t v)
+{
+    return (uint64_t)swap<CTRL>((uint32_t)(v >> 32)) << 32 | swap<CTRL>((uint32_t)v);
+}
+
+__device__ __forceinline__ uint64_t lane_of(uint64_t v, int lane)
+{
+    return (uint64_t)lane_of((uint32_t)(v >> 32), lane) << 32 | lane_of((uint32_t)v, lane);
 }
 
 constexpr int kNext = 0xB1, kPairs = 0x4E, kHalves = 0x141, kRow = 0x140;  // neighbours, pairs, mirrored halves and rows
@@ -171,12 +184,24 @@ __device__ __forceinline__ float softmax_sum(const float* l, float& m, float* e)
 
 __device__ __forceinline__ float sigmoid(float l) { return __builtin_amdgcn_rcpf(1.f + expf(-l)); }
 
-// A lower bound of how far f32 values of c have to be apart for their order to be sure: each
-// is off by less than 64 roundings (softmax: 2 x e^-x of its own term, twice the mean
-// |x| of the sum's, below log E, 2 each of exp and quotient, 24 of the sum; the bias' sum one).
-__device__ __forceinline__ bool near(float above, float below, int terms)
+// Whether two f32 values of c, above >= below, are too near for their order to be sure; in
+// roundings u = 2^-24, with `off` for what two scores can be off by:
+//   sigmoid: 1 + exp and its reciprocal 3, exp's own (1.5 |x| + 2) s (1 - s) below 1: 8 of two
+//   softmax: s <= 1 / z; e^-x: (2.5 |x| + 2) e^-x below 3; z: the mean of 2.5 |x| over the terms
+//            below 2.5 log E, 2, and 22 of its sum; 2 of 1 / z: 94 / z of two
+// and one of |c| each for the bias' sum.
+__device__ __forceinline__ float off_by(bool softmax, float rz) { return softmax ? 128.f * rz : 16.f; }
+
+__device__ __forceinline__ bool near(float above, float below, float off)
 {
-    return !(above - below > 0x1p-17f * (float)terms * (1.f + fabsf(above)));
+    return !(above - below > 0x1p-24f * (off + 4.f * fabsf(above)));
+}
+
+// The same for sums of n of them, whose magnitudes' sums come to `size` in both together: n
+// scores, n roundings of |c| and n - 1 of partial sums.
+__device__ __forceinline__ bool near_sums(float above, float below, float off, int n, float size)
+{
+    return !(above - below > 0x1p-24f * (float)n * (off + 2.f * size));
 }
 
 // The largest key of the wave: its lane (the lowest of equals); 0 if all keys are 0.
@@ -193,27 +218,37 @@ __device__ __forceinline__ uint32_t wave_best(uint32_t hi, uint32_t lo, int& lan
     return top;
 }
 
+__device__ __forceinline__ double from_key(uint64_t k) { return from_order64(k); }
+__device__ __forceinline__ float from_key(uint32_t k) { return from_order32(k); }
+__device__ __forceinline__ uint64_t to_key(double v) { return order64(v); }
+__device__ __forceinline__ uint32_t to_key(float v) { return order32(v); }
+
 // Takes the experts of other than the best groups out (their keys become 0).  `sums`: the
-// groups' sums are of values that may be off; true then if the last group in and the
+// groups' sums are of values that may be `off`; true then if the last group in and the
 // first one out are too near.  WIDE: keys of 64 bits.
 template <int N, bool WIDE>
 __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, unsigned magic, uint64_t* keys, int lane,
-                                            bool sums, uint32_t* hi, uint32_t* lo)
+                                            bool sums, float off, uint32_t* hi, uint32_t* lo)
 {
+    using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
     const int e0 = lane * N, lanes = group_size / N;
     // groups of whole lanes, 1 to 16 of them: the best two by swaps inside the group
-    const bool whole = !WIDE && lanes * N == group_size && lanes <= 16 && (lanes & (lanes - 1)) == 0 && a.group_top <= 2;
-    uint32_t group_hi = 0, group_lo = 0;
+    const bool whole = lanes * N == group_size && lanes <= 16 && (lanes & (lanes - 1)) == 0 && a.group_top <= 2;
+    Key group = 0;
+    float size = 0.f;  // magnitudes of the group's sum
     if (whole) {
-        uint32_t one = hi[0], two = 0;
+        const auto high = [](Key x, Key y) { return x > y ? x : y; };
+        const auto low = [](Key x, Key y) { return x > y ? y : x; };
+        const auto key = [&](int i) { return WIDE ? (Key)((uint64_t)hi[i] << 32 | lo[i]) : (Key)hi[i]; };
+        Key one = key(0), two = 0;
 #pragma unroll
         for (int i = 1; i < N; ++i) {
-            two = max(two, min(one, hi[i]));
-            one = max(one, hi[i]);
+            two = high(two, low(one, key(i)));
+            one = high(one, key(i));
         }
-        const auto merge = [&](uint32_t b1, uint32_t b2) {
-            two = max(max(two, b2), min(one, b1));
-            one = max(one, b1);
+        const auto merge = [&](Key b1, Key b2) {
+            two = high(high(two, b2), low(one, b1));
+            one = high(one, b1);
         };
         if (lanes > 1)
             merge(swap<kNext>(one), swap<kNext>(two));
@@ -223,9 +258,14 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
             merge(swap<kHalves>(one), swap<kHalves>(two));
         if (lanes > 8)
             merge(swap<kRow>(one), swap<kRow>(two));
-        group_hi = one;
-        if (a.group_top == 2 && two != 0)
-            group_hi = order32(from_order32(one) + from_order32(two));
+        group = one;
+        if (a.group_top == 2 && two != 0) {
+            const auto first = from_key(one), second = from_key(two);
+            group = to_key(first + second);
+            size = fabsf((float)first) + fabsf((float)second);
+        } else if (one != 0) {
+            size = fabsf((float)from_key(one));
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -238,8 +278,7 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
             const uint64_t* const of = keys + lane * group_size;
             uint64_t last = ~UINT64_C(0);
             int last_at = -1;
-            double sum = 0;
-            float sum32 = 0.f;
+            std::conditional_t<WIDE, double, float> sum = 0;
             for (int p = 0; p < a.group_top; ++p) {
                 uint64_t best = 0;
                 int at = group_size;
@@ -255,18 +294,14 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
                 }
                 if (best == 0)
                     break;
-                if (WIDE)
-                    sum += from_order64(best);
-                else
-                    sum32 += from_order32((uint32_t)(best >> 32));
+                const auto v = from_key((Key)(WIDE ? best : best >> 32));
+                sum += v;
+                size += fabsf((float)v);
                 last = best;
                 last_at = at;
             }
-            if (last_at >= 0) {
-                const uint64_t k = WIDE ? order64(sum) : a.group_top == 1 ? last : (uint64_t)order32(sum32) << 32;
-                group_hi = (uint32_t)(k >> 32);
-                group_lo = (uint32_t)k;
-            }
+            if (last_at >= 0)
+                group = a.group_top == 1 ? (Key)(WIDE ? last : last >> 32) : to_key(sum);
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     }
@@ -278,14 +313,17 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
         const int own = lane >> shift;
         int rank = own < a.groups ? 0 : 64;
         for (int g = 0; g < a.groups; ++g) {
-            const uint32_t other = lane_of(group_hi, g << shift);
-            rank += other > group_hi || (other == group_hi && g < own);
+            const Key other = lane_of(group, g << shift);
+            rank += other > group || (other == group && g < own);
         }
-        if (sums) {
+        if (!WIDE && sums) {
             const uint64_t in = __ballot(rank == a.top_groups - 1), out = __ballot(rank == a.top_groups);
-            const uint32_t last = in ? lane_of(group_hi, __builtin_ctzll(in)) : 0u;
-            const uint32_t next = out ? lane_of(group_hi, __builtin_ctzll(out)) : 0u;
-            close = last != 0 && next != 0 && near(from_order32(last), from_order32(next), a.group_top);
+            if (in && out) {
+                const int i = __builtin_ctzll(in), o = __builtin_ctzll(out);
+                const uint32_t last = lane_of((uint32_t)group, i), next = lane_of((uint32_t)group, o);
+                close = next != 0 && near_sums(from_order32(last), from_order32(next), off, a.group_top,
+                                               lane_of(size, i) + lane_of(size, o));
+            }
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -295,21 +333,25 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
     }
     // (one lane stands for a group)
     if (whole && (lane & (lanes - 1)) != 0)
-        group_hi = 0;
+        group = 0;
     uint32_t last = 0;
+    float last_size = 0.f;
     for (int p = 0; p <= a.top_groups; ++p) {
         int from;
-        const uint32_t top = wave_best<WIDE>(group_hi, group_lo, from);
+        const uint32_t top = WIDE ? wave_best<true>((uint32_t)((uint64_t)group >> 32), (uint32_t)group, from)
+                                  : wave_best<false>((uint32_t)group, 0u, from);
         if (top == 0)
             break;
         if (p == a.top_groups) {
-            close = sums && near(from_order32(last), from_order32(top), a.group_top);
+            close = !WIDE && sums && near_sums(from_order32(last), from_order32(top), off, a.group_top,
+                                               last_size + lane_of(size, from));
             break;
         }
         kept |= UINT64_C(1) << (from >> shift);
         if (lane == from)
-            group_hi = group_lo = 0;
+            group = 0;
         last = top;
+        last_size = lane_of(size, from);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -324,7 +366,7 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
 // own, equal ones by id, and shifts them down as they are taken.  `sums`: true if two
 // that follow one another, the last one in and the first one out among them, are too near.
 template <int N, bool WIDE>
-__device__ __forceinline__ bool pick(int K, int lane, bool sums, uint32_t* hi, uint32_t* lo, int& mine)
+__device__ __forceinline__ bool pick(int K, int lane, bool sums, float off, uint32_t* hi, uint32_t* lo, int& mine)
 {
     int id[N];
 #pragma unroll
@@ -368,8 +410,9 @@ __device__ __forceinline__ bool pick(int K, int lane, bool sums, uint32_t* hi, u
     }
     if (!sums)
         return false;
-    const uint32_t below = lane == n - 1 ? out : (uint32_t)__shfl_down(top_of, 1);
-    return __ballot(lane < n && below != 0 && near(from_order32((uint32_t)top_of), from_order32(below), 1)) != 0;
+    const uint32_t next = (uint32_t)__shfl_down(top_of, 1);  // (by itself: every lane has to take part)
+    const uint32_t below = lane == n - 1 ? out : next;
+    return __ballot(lane < n && below != 0 && near(from_order32((uint32_t)top_of), from_order32(below), off)) != 0;
 }
 
 }  // namespace
@@ -412,6 +455,7 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
 
     uint32_t hi[N], lo[N];
     bool close = false;
+    float off = 0.f;
     if constexpr (SUMS) {
         // c in f32; what is not finite is left to 64 bits
         if (!softmax)
@@ -419,6 +463,7 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
             for (int i = 0; i < N; ++i)
                 e[i] = __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
         const float rz = softmax ? __builtin_amdgcn_rcpf(z) : 1.f;
+        off = off_by(softmax, rz);
         float odd = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -447,11 +492,11 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
     };
     int mine = -1;
     if (a.groups > 1 && !close)
-        close = keep_groups<N, false>(a, group_size, magic, keys, lane, SUMS, hi, lo);
+        close = keep_groups<N, false>(a, group_size, magic, keys, lane, SUMS, off, hi, lo);
     if (SUMS && !a.bias)
         by_logits();
     if (!close)
-        close = pick<N, false>(a.K, lane, SUMS && a.bias, hi, lo, mine);
+        close = pick<N, false>(a.K, lane, SUMS && a.bias, off, hi, lo, mine);
     if (SUMS && close) {
         double c[N], zd = 0;
 #pragma unroll
@@ -472,10 +517,10 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
             lo[i] = (uint32_t)k;
         }
         if (a.groups > 1)
-            keep_groups<N, true>(a, group_size, magic, keys, lane, false, hi, lo);
+            keep_groups<N, true>(a, group_size, magic, keys, lane, false, 0.f, hi, lo);
         if (!a.bias)
             by_logits();
-        pick<N, true>(a.K, lane, false, hi, lo, mine);
+        pick<N, true>(a.K, lane, false, 0.f, hi, lo, mine);
     }
 
     // lane j the weight of slot j

@@ -83,6 +83,36 @@ def test_groups_of_whole_lanes(run):
                 check(l, got, K, b, None, sigmoid, groups, top_groups, group_top, True, 1.0)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [2, 3])
+def test_groups_whose_biases_cancel(group_top, sigmoid):
+    # sums of small scores and of biases of both signs, next to which float32 cannot see the scores
+    T, E, size = 300, 64, group_top
+    groups = E // size
+    say(f"gate: {groups} groups of cancelling biases")
+    l, _, _, rng = draw((T, groups * size), torch.float32, 7, masked=False)
+    bias = torch.tensor([4096.0, -4096.0, 0.0][:size]).repeat(groups)
+    got = moe.moe_gate(l.cuda(), 4, bias=bias.cuda(), score=moe.MOE_SCORE_SIGMOID if sigmoid else moe.MOE_SCORE_SOFTMAX,
+                       groups=groups, top_groups=max(2, groups // 4), group_top=group_top)
+    check(l, got, 4, bias, None, sigmoid, groups, max(2, groups // 4), group_top, True, 1.0)
+
+
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_near_neighbours_in_every_slot(K):
+    # the slots' values but the last two well apart, and these too near for float32, the higher id ahead
+    say(f"gate: near neighbours in the last of {K} slots")
+    l = torch.full((1, 130), -3.0)
+    bias = torch.zeros(130)
+    for j in range(K - 2):
+        bias[100 + j] = 8192.0 - j
+    l[0, 40], l[0, 41] = 1.0, 1.0 + 2.0 ** -12                # scores 2^-14 apart, next to 4096
+    bias[40:42] = 4096.0
+    want = [100 + j for j in range(K - 2)] + [41, 40]
+    for k in (K - 1, K, K + 1):
+        idx, _ = moe.moe_gate(l.cuda(), k, bias=bias.cuda(), score=moe.MOE_SCORE_SIGMOID)
+        assert idx[0, :K].tolist() == want[:k]
+
+
 def test_ties_go_to_the_lower_id():
     say("ties")
     T, E = 40, 320
