@@ -548,7 +548,14 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
         return;
     char* const out = a.dlogits + t * a.dlogits_ld;
     const int e0 = lane * N;
-    int mine = lane < a.K ? a.idx[t * a.K + lane] : -1;
+    const char* const row = a.logits + t * a.ld;
+    float l[N], given = 0.f;
+    int mine = -1;
+    if (lane < a.K) {
+        mine = a.idx[t * a.K + lane];
+        given = a.w[t * a.K + lane];
+    }
+    load_run<E, N>(row, e0, a.E, l);
     if (mine >= a.E)
         mine = -1;
     float d[N];
@@ -557,14 +564,20 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
         d[i] = 0.f;
     const uint64_t slots = __ballot(mine >= 0);
     if (slots != 0) {
-        const char* const row = a.logits + t * a.ld;
         const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-        float l[N], e[N], m = 0.f, z = 1.f, v = 0.f, g = 0.f;
-        load_run<E, N>(row, e0, a.E, l);
+        float e[N], m = 0.f, z = 1.f, v = 0.f, g = 0.f;
+        float* const table = slot_table + wave * (64 * N);
+        // the slots' logits by way of LDS (a second, dependent load: 14.4 us for 13.5 at 32768
+        // x 384 bf16; the row after its slots, too: 15.0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            table[e0 + i] = l[i];
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         if (mine >= 0) {
-            v = E::load(row + (int64_t)mine * E::SIZE);
-            g = a.scale * a.w[t * a.K + lane];
+            v = table[mine];
+            g = a.scale * given;
         }
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         if (softmax)
             z = softmax_sum<N>(l, m, e);
         const float rz = __builtin_amdgcn_rcpf(z);
@@ -586,7 +599,6 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
         for (int i = 0; i < N; ++i)
             d[i] = softmax ? -q : 0.f;
         // the slots' dp to their experts' lanes by way of LDS, unless an expert is named twice
-        float* const table = slot_table + wave * (64 * N);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             table[e0 + i] = 0.f;

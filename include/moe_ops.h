@@ -205,8 +205,8 @@ int moe_gate(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t dty
  * Gradient of moe_gate's weights with respect to the logits, the choice fixed
  * (bias, groups and mask have done their part in it):
  *   dlogits[t, e] = sum over j of dw[t, j] * d topk_w[t, j] / d l[e]
- * over the slots with 0 <= topk_idx < E (the others' dw is not read); a token with
- * no such slot gets zeros and its logits are not read.  A slot's expert may be
+ * over the slots with 0 <= topk_idx < E (the others' dw counts for nothing); a token
+ * with no such slot gets zeros whatever its logits are.  A slot's expert may be
  * named twice.  dlogits [T, E] in the logits' type, rounded once from f32.
  * Ranges as for moe_gate.  dlogits overlaps nothing.
  */
