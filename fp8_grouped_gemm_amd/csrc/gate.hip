@@ -13,8 +13,13 @@
 // integers in the order of the values (NaN on top, 0 for experts that cannot be
 // chosen), whose maximum over a wave is a handful of instructions.  c and the groups' sums
 // are formed in f32 first: where neighbours of the choice are further apart than f32
-// can be off (all but some of a thousand tokens of ordinary logits), the choice is that of
-// the formula; elsewhere the token's c are formed in 64 bits.
+// can be off (all but a few tokens of ordinary logits), the choice is that of the formula;
+// elsewhere the token's c are formed in 64 bits.
+//
+// Instructions bound it: 8192 tokens of 256 experts, sigmoid and bias, 4 of 8 groups, top-8
+// take 10.8 - 11.9 us of which 10 are the call, 32768 tokens 28.7 (27.3 if none went to 64 bits),
+// where the logits take 7 to read.  The gradient moves 52 MB of 32768 x 384 bf16 in 13.5 us, 3.7
+// TB/s; waves that walk the tokens and load the next one early take 16.0.
 #include "../../include/moe_ops.h"
 #include "ops_internal.h"
 #include "rows_device.h"

@@ -63,6 +63,45 @@ def test_norm_and_router_before_the_fused_forward(tokens):
     assert np.linalg.norm(lu.f64(out) - ref) <= 1e-2 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("T,align", [(1, 16), (45, 16), (45, 1)])
+def test_four_bit_layer(T, align):
+    # a layer of 4-bit experts between the router and the tokens' order, padding rows never written by the activation
+    say(f"4-bit layer, {T} tokens")
+    H, I, E, K = 256, 96, 6, 2
+    g = torch.Generator().manual_seed(T + align)
+    rand = lambda *s: torch.randn(*s, generator=g).cuda()
+    x, logits = rand(T, H).to(BF16), rand(T, E)
+    (w1, w1_sf), (w2, w2_sf) = [[t.view(E, n, -1) for t in moe.moe_quantize_mxfp4(rand(E * n, k).to(BF16) / k ** 0.5)]
+                                for n, k in ((2 * I, H), (H, I))]
+    idx, tw = moe.moe_gate(logits, K)
+    r = planner(idx, E, align)
+    seg = dict(offsets=r["offsets"], counts=r["counts"], slots=T * K)
+    codes, sf = moe.moe_quantize_mxfp4(x)
+    xp, xps = (moe.moe_permute(t, r["row_src"], r["src_row"], r["offsets"]) for t in (codes, sf))
+    gu = moe.moe_gemm_mxfp4(xp, xps, w1, w1_sf, **seg)
+    h = torch.full((gu.shape[0], I), float("nan"), dtype=BF16, device="cuda")
+    moe.moe_swiglu(gu, r["row_src"], r["offsets"], h=h)
+    used = torch.arange(h.shape[0], device="cuda") < r["offsets"][-1]
+    live = used & (r["row_src"] >= 0)
+    want = lu.swiglu(lu.f64(gu[live]))
+    # (bf16 of float32 with at most 128 roundings: the sigmoid's |g| and ten)
+    lu.within(h[live], want, lu.rounded_bound(want, 128 * lu.U32 * abs(want) + 2.0 ** -120, BF16))
+    assert torch.isnan(h[~live]).all()
+    yp = moe.moe_gemm_mxfp4(*moe.moe_quantize_mxfp4(h), w2, w2_sf, **seg)
+    y = moe.moe_unpermute(yp, r["src_row"], T, tw)
+    # the same layer token by token
+    for t in range(T):
+        out = torch.zeros(H, dtype=torch.float64, device="cuda")
+        for j in range(K):
+            e = idx[t, j].item()
+            a = moe.moe_gemm_mxfp4(codes[t:t + 1], sf[t:t + 1], w1[e], w1_sf[e])
+            b = moe.moe_gemm_mxfp4(*moe.moe_quantize_mxfp4(moe.moe_swiglu(a)[0]), w2[e], w2_sf[e])
+            out += tw[t, j].double() * b[0].double()
+        # other tiles add in another order: a bf16 step in gate or up, and a 4-bit code of h beside a border (half of its
+        # value) on the other side, of I of them
+        assert torch.linalg.vector_norm(y[t].double() - out) <= 0.1 * torch.linalg.vector_norm(out) + 1e-3
+
+
 class Layer:
     """Tokens of width H, residual, norm, a router and E experts of inner width I; activations that the
     backward pass needs are kept in 8 bits."""
