@@ -264,7 +264,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
 
     // The thread's pieces of a stage: offsets from its first row, kOut for columns past the
     // matrix.  A buffer ends with the share's last row, so that rows past it (and kOut) read as
-    // zeros; only a piece that holds a row's last columns and more is loaded one by one.
+    // zeros.  A piece that holds a row's last columns reads on into the next row (what it gets goes
+    // to rows of dw that are none) but in a stage where that would pass the end: there it is
+    // loaded one by one.
     constexpr unsigned kOut = 0x80000000u;
     unsigned d_at[kDy], x_at[kX], sf_at[kX];
     int ragged = 0;  // columns of such a piece
@@ -288,7 +290,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
     };
     const auto load = [&](Regs& to) {  // the next stage (zeros past the last)
         const auto db = buffer(dy, bytes(dy_left)), xb = buffer(x, bytes(x_left)), sb = buffer(sf, bytes(sf_left));
-        if (cut_edge && ragged) {
+        if (cut_edge && dy_left < (kStage - 1) * a.dy_ld + 2 * a.N + 14 && ragged) {
 #pragma unroll
             for (int p = 0; p < kDy; ++p) {
                 const int r = (p * kThreads + (int)threadIdx.x) / (BM / 8);

@@ -253,6 +253,22 @@ def test_larger_products_against_the_plain_form(shape, dtype, fmt):
                        torch.where(none.cuda(), old, (old.float() + got).half()))
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 7, 9, 15, 129, 255])
+def test_rows_that_end_inside_a_piece(n):
+    # columns that are no whole eights, around the ends of stages; whole numbers, so that the sums are exact
+    say(f"weight gradient of {n} columns")
+    g = torch.Generator().manual_seed(n)
+    for rows in (1, 7, 8, 63, 64, 65, 66, 71, 72, 73, 127, 128, 129, 136, 200):
+        dy = torch.randint(-8, 9, (rows, n), generator=g).half()
+        codes = torch.randint(0x38, 0x40, (rows, 64), generator=g).to(torch.uint8)
+        sf = torch.full((rows, 2), 127, dtype=torch.uint8)
+        want = torch.from_numpy(lu.f64(dy).T @ lu.E4M3[codes.numpy()]).float()
+        assert torch.equal(moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda()).cpu(), want), rows
+        off = torch.tensor([0, rows // 3, rows // 3, rows], dtype=torch.int32).cuda()
+        got = moe.moe_gemm_wgrad(dy.cuda(), codes.cuda(), sf.cuda(), offsets=off).cpu()
+        assert torch.equal(got[0] + got[2], want) and torch.all(got[1] == 0), rows
+
+
 def test_widest_stride():
     # 130 rows 2^24 elements apart: stages that span all but 2^31 bytes
     say("weight gradient of rows 32 MB apart")
