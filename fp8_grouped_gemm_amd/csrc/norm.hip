@@ -25,10 +25,18 @@ constexpr int kMaxResident = 16384;
 constexpr int kPartials = 256;       // most partial rows of dw
 constexpr int kColumnThreads = 256;
 
-__device__ __forceinline__ float wave_sum(float v)
+// The sum over LANES lanes of a wave, in each of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v)
 {
+    const auto add = [&](uint32_t other) { v += __uint_as_float(other); };
+    add(block_swap<0xB1>(__float_as_uint(v)));   // quad_perm [1,0,3,2]
+    add(block_swap<0x4E>(__float_as_uint(v)));   // quad_perm [2,3,0,1]
+    add(block_swap<0x141>(__float_as_uint(v)));  // row_half_mirror
+    if constexpr (LANES > 8)
+        add(block_swap<0x140>(__float_as_uint(v)));  // row_mirror
 #pragma unroll
-    for (int x = 1; x < 64; x *= 2)
+    for (int x = 16; x < LANES; x *= 2)
         v += __shfl_xor(v, x);
     return v;
 }
@@ -38,7 +46,7 @@ __device__ __forceinline__ float wave_sum(float v)
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red)
 {
-    v = wave_sum(v);
+    v = lanes_sum<TPR < 64 ? TPR : 64>(v);
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0)
             red[threadIdx.x >> 6] = v;
@@ -109,8 +117,13 @@ constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 
 constexpr int kGradThreads = 1024;
 
-// Threads along a row of a width that fits the registers.
-constexpr int row_threads(int width) { return width <= 1024 ? 64 : width <= 4096 ? 256 : width <= 8192 ? 512 : 1024; }
+// Threads along a row of a width that fits the registers: of a narrow one a part of a wave
+// (524288 x 128 bf16: 107 us, the gradient 106; with a wave a row 275 and 228).
+constexpr int row_threads(int width)
+{
+    return width <= 64 ? 8 : width <= 128 ? 16 : width <= 256 ? 32 : width <= 1024 ? 64 : width <= 4096 ? 256
+         : width <= 8192 ? 512 : 1024;
+}
 
 }  // namespace
 
@@ -197,7 +210,7 @@ __device__ __forceinline__ void store_dx(const NormArgs& a, int64_t row, int col
 template <class E, class W, int TPR, int CH, bool DX, bool DW>
 __global__ __launch_bounds__(kGradThreads) void norm_grad(NormArgs a, int wgs)
 {
-    constexpr int ROWS = kGradThreads / TPR;
+    constexpr int ROWS = kGradThreads / TPR, SHARES = ROWS < kGradThreads / 64 ? ROWS : kGradThreads / 64;
     __shared__ float red[2][16];
     __shared__ __attribute__((aligned(16))) float part[DW && ROWS > 1 ? TPR * CH * 8 : 1];
     const int at = threadIdx.x % TPR, group = threadIdx.x / TPR;
@@ -255,9 +268,19 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad(NormArgs a, int wgs)
         }
     }
     if (DW) {
-        if constexpr (ROWS > 1) {
-            for (int r = 0; r < ROWS - 1; ++r) {
-                if (group == r)
+        // (rows that share a wave first)
+#pragma unroll
+        for (int x = TPR; x < 64; x *= 2)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[c][i] += __shfl_xor(acc[c][i], x);
+        const int own = TPR < 64 ? threadIdx.x / 64 : group;
+        const bool first = TPR >= 64 || threadIdx.x % 64 < TPR;
+        if constexpr (SHARES > 1) {
+            for (int r = 0; r < SHARES - 1; ++r) {
+                if (own == r && first)
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -267,13 +290,13 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad(NormArgs a, int wgs)
                         }
                 __syncthreads();
             }
-            if (group != ROWS - 1)
-                return;
         }
+        if (own != SHARES - 1 || !first)
+            return;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int col = (c * TPR + at) * 8;
-            if constexpr (ROWS > 1)
+            if constexpr (SHARES > 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     acc[c][i] += part[col + i];
@@ -432,6 +455,12 @@ template <class E, class W>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s)
 {
     const auto fills = [&](int threads) { return a.width <= threads * 8 && a.width * 4 >= threads * 8 * 3; };
+    if (a.width <= 64)
+        return launch_rows<E, W, 8, 1>(a, s);
+    if (a.width <= 128)
+        return launch_rows<E, W, 16, 1>(a, s);
+    if (a.width <= 256)
+        return launch_rows<E, W, 32, 1>(a, s);
     if (a.width <= 512)
         return launch_rows<E, W, 64, 1>(a, s);
     if (a.width <= 1024)
@@ -454,6 +483,12 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s)
 template <class E, class W>
 hipError_t launch_back(const NormArgs& a, hipStream_t s)
 {
+    if (a.width <= 64)
+        return launch_grad<E, W, 8, 1>(a, s);
+    if (a.width <= 128)
+        return launch_grad<E, W, 16, 1>(a, s);
+    if (a.width <= 256)
+        return launch_grad<E, W, 32, 1>(a, s);
     if (a.width <= 512)
         return launch_grad<E, W, 64, 1>(a, s);
     if (a.width <= 1024)

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 # rows, width: each kernel's widths and their edges
 SHAPES = [(1, 1), (3, 7), (5, 128), (9, 511), (4, 512), (7, 515), (6, 1024), (3, 1025), (11, 1280), (5, 2048),
           (2, 2049), (130, 4096), (3, 4104), (9, 7168), (2, 8191), (3, 8320), (2, 16384), (2, 16385), (3, 20480),
-          (700, 96)]
+          (700, 96), (301, 64), (45, 65), (1000, 200), (77, 256), (33, 257), (40000, 32), (9000, 128)]
 EPS = 1e-5
 
 
