@@ -8,8 +8,9 @@
 // (dp as a sum of differences: g_j - sum g p / D loses everything where one slot
 // holds all the weight; without renorm dp_j = g_j, q = sum g p).
 //
-// One wave per token, each lane a run of N adjacent experts in registers, so that the
-// lowest lane holding a maximum also holds the lowest id.  Values are compared as
+// One wave per token, each lane a run of N adjacent experts of a group in registers, a group's
+// runs in 1 to 32 lanes (a power of two), so that the lowest lane holding a maximum also holds
+// the lowest id and a group's best are a few lane exchanges away.  Values are compared as
 // integers in the order of the values (NaN on top, 0 for experts that cannot be
 // chosen), whose maximum over a wave is a handful of instructions.  c and the groups' sums
 // are formed in f32 first: where neighbours of the choice are further apart than f32
@@ -228,17 +229,23 @@ __device__ __forceinline__ float from_key(uint32_t k) { return from_order32(k); 
 __device__ __forceinline__ uint64_t to_key(double v) { return order64(v); }
 __device__ __forceinline__ uint32_t to_key(float v) { return order32(v); }
 
+// Where the experts lie.  shift < 6: a group's in 1 << shift lanes, its first N in the first
+// of them; 6: N adjacent ones in each lane, whatever their groups.
+struct Layout {
+    int shift, group_size;
+    unsigned magic;  // e / group_size = e * magic >> 20
+};
+
 // Takes the experts of other than the best groups out (their keys become 0).  `sums`: the
 // groups' sums are of values that may be `off`; true then if the last group in and the
 // first one out are too near.  WIDE: keys of 64 bits.
 template <int N, bool WIDE>
-__device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, unsigned magic, uint64_t* keys, int lane,
-                                            bool sums, float off, uint32_t* hi, uint32_t* lo)
+__device__ __forceinline__ bool keep_groups(const GateArgs& a, const Layout& p, uint64_t* keys, int lane, bool sums,
+                                            float off, uint32_t* hi, uint32_t* lo)
 {
     using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
-    const int e0 = lane * N, lanes = group_size / N;
-    // groups of whole lanes, 1 to 16 of them: the best two by swaps inside the group
-    const bool whole = lanes * N == group_size && lanes <= 16 && (lanes & (lanes - 1)) == 0 && a.group_top <= 2;
+    const bool whole = p.shift < 6;
+    const int e0 = lane * N, lanes = 1 << p.shift, group_size = p.group_size;  // (e0: where not whole)
     Key group = 0;
     float size = 0.f;  // magnitudes of the group's sum
     if (whole) {
@@ -263,6 +270,10 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
             merge(swap<kHalves>(one), swap<kHalves>(two));
         if (lanes > 8)
             merge(swap<kRow>(one), swap<kRow>(two));
+        if (lanes > 16) {
+            const Key b1 = (Key)__shfl_xor((unsigned long long)one, 16), b2 = (Key)__shfl_xor((unsigned long long)two, 16);
+            merge(b1, b2);
+        }
         group = one;
         if (a.group_top == 2 && two != 0) {
             const auto first = from_key(one), second = from_key(two);
@@ -310,7 +321,7 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     }
-    const int shift = whole ? __builtin_ctz(lanes) : 0;
+    const int shift = whole ? p.shift : 0;
     uint64_t kept = 0;
     bool close = false;
     if (whole && a.groups <= 16) {
@@ -360,8 +371,8 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const unsigned g = whole ? (unsigned)lane >> shift : (unsigned)(e0 + i) * magic >> 20;  // (e0 + i) / group_size
-        if (e0 + i >= a.E || !(kept >> (g & 63) & 1))
+        const unsigned g = whole ? (unsigned)lane >> shift : (unsigned)(e0 + i) * p.magic >> 20;  // (e0 + i) / group_size
+        if ((!whole && e0 + i >= a.E) || !(kept >> (g & 63) & 1))
             hi[i] = lo[i] = 0;
     }
     return close;
@@ -371,12 +382,12 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int group_size, u
 // own, equal ones by id, and shifts them down as they are taken.  `sums`: true if two
 // that follow one another, the last one in and the first one out among them, are too near.
 template <int N, bool WIDE>
-__device__ __forceinline__ bool pick(int K, int lane, bool sums, float off, uint32_t* hi, uint32_t* lo, int& mine)
+__device__ __forceinline__ bool pick(int K, int lane, int e0, bool sums, float off, uint32_t* hi, uint32_t* lo, int& mine)
 {
     int id[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        id[i] = i;
+        id[i] = e0 + i;
 #pragma unroll
     for (int phase = 0; phase < N; ++phase)
 #pragma unroll
@@ -401,7 +412,7 @@ __device__ __forceinline__ bool pick(int K, int lane, bool sums, float off, uint
         out = wave_best<WIDE>(hi[0], lo[0], from);
         if (out == 0 || n == K)
             break;
-        const int taken = from * N + (int)lane_of((uint32_t)id[0], from);
+        const int taken = (int)lane_of((uint32_t)id[0], from);
         mine = lane == n ? taken : mine;
         top_of = lane == n ? (int)out : top_of;
         if (lane == from) {
@@ -423,9 +434,10 @@ __device__ __forceinline__ bool pick(int K, int lane, bool sums, float off, uint
 }  // namespace
 
 // SUMS: the choice, or the groups', goes by sums that f32 rounds (a bias, or more than
-// one expert standing for a group).  LDS: E keys of 8 bytes per wave with groups.
+// one expert standing for a group).  LDS: E keys of 8 bytes per wave with groups that do not
+// lie in lanes of their own.
 template <class E, int N, bool SUMS>
-__global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_size, unsigned magic)
+__global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, Layout p)
 {
     extern __shared__ uint64_t group_keys[];
     const int lane = threadIdx.x & 63;
@@ -444,14 +456,16 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
     }
     uint64_t* const keys = group_keys + wave * a.E;
     const char* const row = a.logits + t * a.ld;
-    const int e0 = lane * N;
+    const int group = lane >> p.shift, first = group * p.group_size;  // (shift 6: 0)
+    const int e0 = first + (lane & ((1 << p.shift) - 1)) * N;
+    const int end = p.shift == 6 ? a.E : group < a.groups ? first + p.group_size : 0;
     float l[N], e[N], b[N];
-    load_run<E, N>(row, e0, a.E, l);
+    load_run<E, N>(row, e0, end, l);
 #pragma unroll
     for (int i = 0; i < N; ++i)
         b[i] = 0.f;
     if (SUMS && a.bias) {
-        load_run<F32, N>(reinterpret_cast<const char*>(a.bias), e0, a.E, b);
+        load_run<F32, N>(reinterpret_cast<const char*>(a.bias), e0, end, b);
     }
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
     float m = 0.f, z = 1.f;
@@ -497,11 +511,11 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
     };
     int mine = -1;
     if (a.groups > 1 && !close)
-        close = keep_groups<N, false>(a, group_size, magic, keys, lane, SUMS, off, hi, lo);
+        close = keep_groups<N, false>(a, p, keys, lane, SUMS, off, hi, lo);
     if (SUMS && !a.bias)
         by_logits();
     if (!close)
-        close = pick<N, false>(a.K, lane, SUMS && a.bias, off, hi, lo, mine);
+        close = pick<N, false>(a.K, lane, e0, SUMS && a.bias, off, hi, lo, mine);
     if (SUMS && close) {
         double c[N], zd = 0;
 #pragma unroll
@@ -522,10 +536,10 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, int group_si
             lo[i] = (uint32_t)k;
         }
         if (a.groups > 1)
-            keep_groups<N, true>(a, group_size, magic, keys, lane, false, 0.f, hi, lo);
+            keep_groups<N, true>(a, p, keys, lane, false, 0.f, hi, lo);
         if (!a.bias)
             by_logits();
-        pick<N, true>(a.K, lane, false, 0.f, hi, lo, mine);
+        pick<N, true>(a.K, lane, e0, false, 0.f, hi, lo, mine);
     }
 
     // lane j the weight of slot j
@@ -650,54 +664,70 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
 namespace {
 
 template <class E, int N>
-hipError_t launch(const GateArgs& a, bool back, hipStream_t s)
+hipError_t launch(const GateArgs& a, const Layout* p, hipStream_t s)
 {
     const dim3 grid = grid_of(((int64_t)a.T + kWaves - 1) / kWaves), block(kThreads);
-    if (back) {
+    if (!p) {
         hipLaunchKernelGGL((gate_grad<E, N>), grid, block, 0, s, a);
         return hipGetLastError();
     }
-    const int size = a.E / a.groups;
-    // e / size for e < 1024 and size <= 1024: the error, e (magic - 2^20 / size) / 2^20, stays below 1 / size
-    const unsigned magic = ((1u << 20) + size - 1) / size;
-    const size_t lds = a.groups > 1 ? (size_t)kWaves * a.E * 8 : 0;
+    const size_t lds = a.groups > 1 && p->shift == 6 ? (size_t)kWaves * a.E * 8 : 0;
     const bool sums = a.bias || (a.groups > 1 && a.group_top > 1);
     const auto kernel = sums ? gate_choose<E, N, true> : gate_choose<E, N, false>;
-    hipLaunchKernelGGL(kernel, grid, block, lds, s, a, size, magic);
+    hipLaunchKernelGGL(kernel, grid, block, lds, s, a, *p);
     return hipGetLastError();
 }
 
+// n: experts a lane takes; p: the choice's layout, null for the gradient.
 template <class E>
-hipError_t launch_run(const GateArgs& a, bool back, hipStream_t s)
+hipError_t launch_run(const GateArgs& a, int n, const Layout* p, hipStream_t s)
 {
-    const int n = (a.E + 63) / 64;
     if (n <= 1)
-        return launch<E, 1>(a, back, s);
+        return launch<E, 1>(a, p, s);
     if (n <= 2)
-        return launch<E, 2>(a, back, s);
+        return launch<E, 2>(a, p, s);
     if (n <= 4)
-        return launch<E, 4>(a, back, s);
+        return launch<E, 4>(a, p, s);
     if (n <= 6)
-        return launch<E, 6>(a, back, s);
+        return launch<E, 6>(a, p, s);
     if (n <= 8)
-        return launch<E, 8>(a, back, s);
-    return launch<E, 16>(a, back, s);
+        return launch<E, 8>(a, p, s);
+    return launch<E, 16>(a, p, s);
 }
 
-hipError_t launch_type(const GateArgs& a, bool back, hipStream_t s)
+hipError_t launch_type(const GateArgs& a, int n, const Layout* p, hipStream_t s)
 {
     switch (a.dtype) {
-    case MOE_DTYPE_BF16: return launch_run<Bf16>(a, back, s);
-    case MOE_DTYPE_F16: return launch_run<F16>(a, back, s);
-    case MOE_DTYPE_F32: return launch_run<F32>(a, back, s);
+    case MOE_DTYPE_BF16: return launch_run<Bf16>(a, n, p, s);
+    case MOE_DTYPE_F16: return launch_run<F16>(a, n, p, s);
+    case MOE_DTYPE_F32: return launch_run<F32>(a, n, p, s);
     default: return hipErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-hipError_t launch_gate(const GateArgs& a, hipStream_t s) { return launch_type(a, false, s); }
+hipError_t launch_gate(const GateArgs& a, hipStream_t s)
+{
+    const int size = a.E / a.groups;
+    // e / size for e < 1024 and size <= 1024: the error, e (magic - 2^20 / size) / 2^20, stays below 1 / size
+    Layout p{6, size, ((1u << 20) + size - 1) / size};
+    int n = (a.E + 63) / 64;
+    // Groups in lanes of their own, where runs of 16 experts suffice and at most two experts stand
+    // for a group (32768 tokens of 160 experts in 8 groups 24 us, by way of LDS 45 to 70).
+    if (a.groups > 1 && a.group_top <= 2) {
+        int shift = 5;
+        while (a.groups << shift > 64)
+            --shift;
+        const int run = (size + (1 << shift) - 1) >> shift;
+        if (run <= 16) {
+            p.shift = shift;
+            n = run;
+        }
+    }
+    return launch_type(a, n, &p, s);
+}
 
-hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t s) { return launch_type(a, true, s); }
+hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t s) { return launch_type(a, (a.E + 63) / 64, nullptr, s); }
 
 }  // namespace moe
