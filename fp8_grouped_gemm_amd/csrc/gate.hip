@@ -20,7 +20,10 @@
 // Instructions bound it: 8192 tokens of 256 experts, sigmoid and bias, 4 of 8 groups, top-8
 // take 10.8 - 11.9 us of which 10 are the call, 32768 tokens 28.7 (27.3 if none went to 64 bits),
 // where the logits take 7 to read.  The gradient moves 52 MB of 32768 x 384 bf16 in 13.5 us, 3.7
-// TB/s; waves that walk the tokens and load the next one early take 16.0.
+// TB/s; waves that walk the tokens and load the next one early take 16.0.  Runs of at most eight
+// experts make most calls; 32768 tokens of 512 experts, 8 groups, top-8: 45 us, of 1024 with
+// runs of 16 93, of 1000 in 10 groups with runs of 25 (in instances for 32) 430: a run's sort grows
+// with its square.
 #include "../../include/moe_ops.h"
 #include "ops_internal.h"
 #include "rows_device.h"
@@ -229,29 +232,27 @@ __device__ __forceinline__ float from_key(uint32_t k) { return from_order32(k); 
 __device__ __forceinline__ uint64_t to_key(double v) { return order64(v); }
 __device__ __forceinline__ uint32_t to_key(float v) { return order32(v); }
 
-// Where the experts lie.  shift < 6: a group's in 1 << shift lanes, its first N in the first
-// of them; 6: N adjacent ones in each lane, whatever their groups.
+// Where the experts lie: a group's in 1 << shift lanes, its first N in the first of them.
 struct Layout {
     int shift, group_size;
-    unsigned magic;  // e / group_size = e * magic >> 20
 };
 
 // Takes the experts of other than the best groups out (their keys become 0).  `sums`: the
 // groups' sums are of values that may be `off`; true then if the last group in and the
 // first one out are too near.  WIDE: keys of 64 bits.
 template <int N, bool WIDE>
-__device__ __forceinline__ bool keep_groups(const GateArgs& a, const Layout& p, uint64_t* keys, int lane, bool sums,
-                                            float off, uint32_t* hi, uint32_t* lo)
+__device__ __forceinline__ bool keep_groups(const GateArgs& a, int shift, int lane, bool sums, float off, uint32_t* hi,
+                                            uint32_t* lo)
 {
     using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
-    const bool whole = p.shift < 6;
-    const int e0 = lane * N, lanes = 1 << p.shift, group_size = p.group_size;  // (e0: where not whole)
+    const int lanes = 1 << shift;
+    const auto high = [](Key x, Key y) { return x > y ? x : y; };
+    const auto low = [](Key x, Key y) { return x > y ? y : x; };
+    const auto key = [&](int i) { return WIDE ? (Key)((uint64_t)hi[i] << 32 | lo[i]) : (Key)hi[i]; };
+    const auto far = [](Key x) { return (Key)__shfl_xor((unsigned long long)x, 16); };
     Key group = 0;
     float size = 0.f;  // magnitudes of the group's sum
-    if (whole) {
-        const auto high = [](Key x, Key y) { return x > y ? x : y; };
-        const auto low = [](Key x, Key y) { return x > y ? y : x; };
-        const auto key = [&](int i) { return WIDE ? (Key)((uint64_t)hi[i] << 32 | lo[i]) : (Key)hi[i]; };
+    if (a.group_top <= 2) {
         Key one = key(0), two = 0;
 #pragma unroll
         for (int i = 1; i < N; ++i) {
@@ -271,7 +272,7 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, const Layout& p, 
         if (lanes > 8)
             merge(swap<kRow>(one), swap<kRow>(two));
         if (lanes > 16) {
-            const Key b1 = (Key)__shfl_xor((unsigned long long)one, 16), b2 = (Key)__shfl_xor((unsigned long long)two, 16);
+            const Key b1 = far(one), b2 = far(two);
             merge(b1, b2);
         }
         group = one;
@@ -283,50 +284,52 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, const Layout& p, 
             size = fabsf((float)from_key(one));
         }
     } else {
+        // the largest of what is left, as often as asked for; the lowest lane that holds it gives it up
+        Key left[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (e0 + i < a.E)
-                keys[e0 + i] = (uint64_t)hi[i] << 32 | (WIDE ? lo[i] : 0u);
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        // lane g sums group g's best: each pass finds the largest key behind the
-        // last one's (key descending, id ascending)
-        if (lane < a.groups) {
-            const uint64_t* const of = keys + lane * group_size;
-            uint64_t last = ~UINT64_C(0);
-            int last_at = -1;
-            std::conditional_t<WIDE, double, float> sum = 0;
-            for (int p = 0; p < a.group_top; ++p) {
-                uint64_t best = 0;
-                int at = group_size;
-                int j = lane % group_size;  // (lanes start apart: their keys lie in different banks)
-                for (int n = 0; n < group_size; ++n) {
-                    const uint64_t k = of[j];
-                    const bool later = k < last || (k == last && j > last_at);
-                    if (later && (k > best || (k == best && j < at))) {
-                        best = k;
-                        at = j;
-                    }
-                    j = j + 1 == group_size ? 0 : j + 1;
-                }
-                if (best == 0)
-                    break;
-                const auto v = from_key((Key)(WIDE ? best : best >> 32));
+            left[i] = key(i);
+        std::conditional_t<WIDE, double, float> sum = 0;
+        bool any = false;
+        for (int p = 0; p < a.group_top; ++p) {
+            Key own = left[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i)
+                own = high(own, left[i]);
+            Key top = own;
+            if (lanes > 1)
+                top = high(top, swap<kNext>(top));
+            if (lanes > 2)
+                top = high(top, swap<kPairs>(top));
+            if (lanes > 4)
+                top = high(top, swap<kHalves>(top));
+            if (lanes > 8)
+                top = high(top, swap<kRow>(top));
+            if (lanes > 16) {
+                const Key other = far(top);
+                top = high(top, other);
+            }
+            const uint64_t who = __ballot(own == top) >> (lane & ~(lanes - 1));
+            bool gives = __builtin_ctzll(who) == (lane & (lanes - 1));
+            if (top != 0) {
+                const auto v = from_key(top);
                 sum += v;
                 size += fabsf((float)v);
-                last = best;
-                last_at = at;
+                any = true;
             }
-            if (last_at >= 0)
-                group = a.group_top == 1 ? (Key)(WIDE ? last : last >> 32) : to_key(sum);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool this_one = gives && left[i] == top;
+                left[i] = this_one ? 0 : left[i];
+                gives = gives && !this_one;
+            }
         }
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        group = any ? to_key(sum) : 0;
     }
-    const int shift = whole ? p.shift : 0;
-    uint64_t kept = 0;
     bool close = false;
-    if (whole && a.groups <= 16) {
+    const int own = lane >> shift;
+    if (a.groups <= 16) {
         // a group's rank: how many are above it
-        const int own = lane >> shift;
         int rank = own < a.groups ? 0 : 64;
         for (int g = 0; g < a.groups; ++g) {
             const Key other = lane_of(group, g << shift);
@@ -348,8 +351,9 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, const Layout& p, 
         return close;
     }
     // (one lane stands for a group)
-    if (whole && (lane & (lanes - 1)) != 0)
+    if ((lane & (lanes - 1)) != 0)
         group = 0;
+    uint64_t kept = 0;
     uint32_t last = 0;
     float last_size = 0.f;
     for (int p = 0; p <= a.top_groups; ++p) {
@@ -370,11 +374,9 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, const Layout& p, 
         last_size = lane_of(size, from);
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const unsigned g = whole ? (unsigned)lane >> shift : (unsigned)(e0 + i) * p.magic >> 20;  // (e0 + i) / group_size
-        if ((!whole && e0 + i >= a.E) || !(kept >> (g & 63) & 1))
+    for (int i = 0; i < N; ++i)
+        if (!(kept >> own & 1))
             hi[i] = lo[i] = 0;
-    }
     return close;
 }
 
@@ -434,12 +436,10 @@ __device__ __forceinline__ bool pick(int K, int lane, int e0, bool sums, float o
 }  // namespace
 
 // SUMS: the choice, or the groups', goes by sums that f32 rounds (a bias, or more than
-// one expert standing for a group).  LDS: E keys of 8 bytes per wave with groups that do not
-// lie in lanes of their own.
+// one expert standing for a group).
 template <class E, int N, bool SUMS>
 __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, Layout p)
 {
-    extern __shared__ uint64_t group_keys[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)workgroup() * kWaves + wave;
@@ -454,11 +454,10 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, Layout p)
         }
         return;
     }
-    uint64_t* const keys = group_keys + wave * a.E;
     const char* const row = a.logits + t * a.ld;
-    const int group = lane >> p.shift, first = group * p.group_size;  // (shift 6: 0)
+    const int group = lane >> p.shift, first = group * p.group_size;
     const int e0 = first + (lane & ((1 << p.shift) - 1)) * N;
-    const int end = p.shift == 6 ? a.E : group < a.groups ? first + p.group_size : 0;
+    const int end = group < a.groups ? first + p.group_size : 0;
     float l[N], e[N], b[N];
     load_run<E, N>(row, e0, end, l);
 #pragma unroll
@@ -511,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, Layout p)
     };
     int mine = -1;
     if (a.groups > 1 && !close)
-        close = keep_groups<N, false>(a, p, keys, lane, SUMS, off, hi, lo);
+        close = keep_groups<N, false>(a, p.shift, lane, SUMS, off, hi, lo);
     if (SUMS && !a.bias)
         by_logits();
     if (!close)
@@ -536,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void gate_choose(GateArgs a, Layout p)
             lo[i] = (uint32_t)k;
         }
         if (a.groups > 1)
-            keep_groups<N, true>(a, p, keys, lane, false, 0.f, hi, lo);
+            keep_groups<N, true>(a, p.shift, lane, false, 0.f, hi, lo);
         if (!a.bias)
             by_logits();
         pick<N, true>(a.K, lane, e0, false, 0.f, hi, lo, mine);
@@ -668,13 +667,15 @@ hipError_t launch(const GateArgs& a, const Layout* p, hipStream_t s)
 {
     const dim3 grid = grid_of(((int64_t)a.T + kWaves - 1) / kWaves), block(kThreads);
     if (!p) {
-        hipLaunchKernelGGL((gate_grad<E, N>), grid, block, 0, s, a);
-        return hipGetLastError();
+        if constexpr (N <= 16) {  // (1024 experts over the wave)
+            hipLaunchKernelGGL((gate_grad<E, N>), grid, block, 0, s, a);
+            return hipGetLastError();
+        }
+        return hipErrorInvalidValue;
     }
-    const size_t lds = a.groups > 1 && p->shift == 6 ? (size_t)kWaves * a.E * 8 : 0;
     const bool sums = a.bias || (a.groups > 1 && a.group_top > 1);
     const auto kernel = sums ? gate_choose<E, N, true> : gate_choose<E, N, false>;
-    hipLaunchKernelGGL(kernel, grid, block, lds, s, a, *p);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, *p);
     return hipGetLastError();
 }
 
@@ -692,7 +693,10 @@ hipError_t launch_run(const GateArgs& a, int n, const Layout* p, hipStream_t s)
         return launch<E, 6>(a, p, s);
     if (n <= 8)
         return launch<E, 8>(a, p, s);
-    return launch<E, 16>(a, p, s);
+    if (n <= 16)
+        return launch<E, 16>(a, p, s);
+    // (many experts in a number of groups that leaves lanes without any: at most 31 of them)
+    return launch<E, 32>(a, p, s);
 }
 
 hipError_t launch_type(const GateArgs& a, int n, const Layout* p, hipStream_t s)
@@ -709,23 +713,10 @@ hipError_t launch_type(const GateArgs& a, int n, const Layout* p, hipStream_t s)
 
 hipError_t launch_gate(const GateArgs& a, hipStream_t s)
 {
-    const int size = a.E / a.groups;
-    // e / size for e < 1024 and size <= 1024: the error, e (magic - 2^20 / size) / 2^20, stays below 1 / size
-    Layout p{6, size, ((1u << 20) + size - 1) / size};
-    int n = (a.E + 63) / 64;
-    // Groups in lanes of their own, where runs of 16 experts suffice and at most two experts stand
-    // for a group (32768 tokens of 160 experts in 8 groups 24 us, by way of LDS 45 to 70).
-    if (a.groups > 1 && a.group_top <= 2) {
-        int shift = 5;
-        while (a.groups << shift > 64)
-            --shift;
-        const int run = (size + (1 << shift) - 1) >> shift;
-        if (run <= 16) {
-            p.shift = shift;
-            n = run;
-        }
-    }
-    return launch_type(a, n, &p, s);
+    Layout p{6, a.E / a.groups};
+    while (a.groups << p.shift > 64)
+        --p.shift;
+    return launch_type(a, (p.group_size + (1 << p.shift) - 1) >> p.shift, &p, s);
 }
 
 hipError_t launch_gate_bwd(const GateArgs& a, hipStream_t s) { return launch_type(a, (a.E + 63) / 64, nullptr, s); }
