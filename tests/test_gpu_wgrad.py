@@ -269,6 +269,21 @@ def test_rows_that_end_inside_a_piece(n):
         assert torch.equal(got[0] + got[2], want) and torch.all(got[1] == 0), rows
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+def test_accumulation_at_odd_addresses_and_edges(out):
+    say(f"weight gradient added to {out}")
+    for R, n, k in ((40, 5, 32), (70, 131, 96), (300, 300, 288)):
+        dy, codes, sf, _ = make((R, 0, n, k, 1), torch.bfloat16, 1, 8)
+        d = (dy.cuda(), codes.cuda(), sf.cuda())
+        got = moe.moe_gemm_wgrad(*d)
+        buf = torch.full((n * k + 2,), 7.0, dtype=out, device="cuda")
+        buf[1:-1].normal_()
+        old = buf.clone()
+        moe.moe_gemm_wgrad(*d, out=buf[1:-1].view(n, k), accumulate=True)
+        assert torch.equal(buf[1:-1].view(n, k), (old[1:-1].view(n, k).float() + got).to(out))
+        assert buf[0] == 7 and buf[-1] == 7
+
+
 def test_widest_stride():
     # 130 rows 2^24 elements apart: stages that span all but 2^31 bytes
     say("weight gradient of rows 32 MB apart")
