@@ -18,12 +18,11 @@
 // elsewhere the token's c are formed in 64 bits.
 //
 // Instructions bound it: 8192 tokens of 256 experts, sigmoid and bias, 4 of 8 groups, top-8
-// take 10.8 - 11.9 us of which 10 are the call, 32768 tokens 28.7 (27.3 if none went to 64 bits),
-// where the logits take 7 to read.  The gradient moves 52 MB of 32768 x 384 bf16 in 13.5 us, 3.7
-// TB/s; waves that walk the tokens and load the next one early take 16.0.  Runs of at most eight
-// experts make most calls; 32768 tokens of 512 experts, 8 groups, top-8: 45 us, of 1024 with
-// runs of 16 93, of 1000 in 10 groups with runs of 25 (in instances for 32) 430: a run's sort grows
-// with its square.
+// take 11.1 us of which 10 are the call, 32768 tokens 30.3, where the logits take 7 to read.  The
+// gradient moves 52 MB of 32768 x 384 bf16 in 13.5 us, 3.7 TB/s; waves that walk the tokens and
+// load the next one early take 16.0.  Runs of at most eight experts make most calls; 32768 tokens
+// of 512 experts, 8 groups, top-8: 47 - 49 us, of 1024 with runs of 16 92, of 1000 in 10 groups with
+// runs of 25 (in instances for 32) 410 - 455: a run's sort grows with its square.
 #include "../../include/moe_ops.h"
 #include "ops_internal.h"
 #include "rows_device.h"
@@ -206,11 +205,18 @@ __device__ __forceinline__ bool near(float above, float below, float off)
     return !(above - below > 0x1p-24f * (off + 4.f * fabsf(above)));
 }
 
-// The same for sums of n of them, whose magnitudes' sums come to `size` in both together: n
-// scores, n roundings of |c| and n - 1 of partial sums.
-__device__ __forceinline__ bool near_sums(float above, float below, float off, int n, float size)
+// Whether f32 may have ranked a group that is `in` above one that is not and ought to be: `sum` is
+// that of the lane's group, `any` whether it has one.  Every group has its own error, as what is
+// left of large terms that cancel is wrong by their size, and one that is far off may stand
+// anywhere in the ranking.  In u, of n terms whose magnitudes come to `size`: off / 2 of each
+// score, n roundings of |c|, n - 1 of partial sums, one of the bound formed here.
+__device__ __forceinline__ bool near_sums(bool any, bool in, float sum, float off, int n, float size)
 {
-    return !(above - below > 0x1p-24f * (float)n * (off + 2.f * size));
+    const float err = 0x1p-24f * (float)n * (0.5f * off + 3.f * size), least = sum - err, most = sum + err;
+    // (a bound that is NaN outdoes all others, comes back as NaN and compares as near)
+    const uint32_t worst = wave_max(any && in ? (least != least ? 0xFFFFFFFFu : ~order32(least)) : 0u);
+    const uint32_t best = wave_max(any && !in ? order32(most) : 0u);
+    return worst != 0 && best != 0 && !(from_order32(~worst) > from_order32(best));
 }
 
 // The largest key of the wave: its lane (the lowest of equals); 0 if all keys are 0.
@@ -238,8 +244,8 @@ struct Layout {
 };
 
 // Takes the experts of other than the best groups out (their keys become 0).  `sums`: the
-// groups' sums are of values that may be `off`; true then if the last group in and the
-// first one out are too near.  WIDE: keys of 64 bits.
+// groups' sums are of values that may be `off`; true then if another choice of groups may be the
+// formula's.  WIDE: keys of 64 bits.
 template <int N, bool WIDE>
 __device__ __forceinline__ bool keep_groups(const GateArgs& a, int shift, int lane, bool sums, float off, uint32_t* hi,
                                             uint32_t* lo)
@@ -335,15 +341,8 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int shift, int la
             const Key other = lane_of(group, g << shift);
             rank += other > group || (other == group && g < own);
         }
-        if (!WIDE && sums) {
-            const uint64_t in = __ballot(rank == a.top_groups - 1), out = __ballot(rank == a.top_groups);
-            if (in && out) {
-                const int i = __builtin_ctzll(in), o = __builtin_ctzll(out);
-                const uint32_t last = lane_of((uint32_t)group, i), next = lane_of((uint32_t)group, o);
-                close = next != 0 && near_sums(from_order32(last), from_order32(next), off, a.group_top,
-                                               lane_of(size, i) + lane_of(size, o));
-            }
-        }
+        if (!WIDE && sums)
+            close = near_sums(group != 0, rank < a.top_groups, from_order32((uint32_t)group), off, a.group_top, size);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (rank >= a.top_groups)
@@ -351,28 +350,20 @@ __device__ __forceinline__ bool keep_groups(const GateArgs& a, int shift, int la
         return close;
     }
     // (one lane stands for a group)
-    if ((lane & (lanes - 1)) != 0)
-        group = 0;
+    Key left = (lane & (lanes - 1)) != 0 ? (Key)0 : group;
     uint64_t kept = 0;
-    uint32_t last = 0;
-    float last_size = 0.f;
-    for (int p = 0; p <= a.top_groups; ++p) {
+    for (int p = 0; p < a.top_groups; ++p) {
         int from;
-        const uint32_t top = WIDE ? wave_best<true>((uint32_t)((uint64_t)group >> 32), (uint32_t)group, from)
-                                  : wave_best<false>((uint32_t)group, 0u, from);
+        const uint32_t top = WIDE ? wave_best<true>((uint32_t)((uint64_t)left >> 32), (uint32_t)left, from)
+                                  : wave_best<false>((uint32_t)left, 0u, from);
         if (top == 0)
             break;
-        if (p == a.top_groups) {
-            close = !WIDE && sums && near_sums(from_order32(last), from_order32(top), off, a.group_top,
-                                               last_size + lane_of(size, from));
-            break;
-        }
         kept |= UINT64_C(1) << (from >> shift);
         if (lane == from)
-            group = 0;
-        last = top;
-        last_size = lane_of(size, from);
+            left = 0;
     }
+    if (!WIDE && sums)
+        close = near_sums(group != 0, kept >> own & 1, from_order32((uint32_t)group), off, a.group_top, size);
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (!(kept >> own & 1))
