@@ -595,14 +595,15 @@ __global__ __launch_bounds__(kThreads) void gate_grad(GateArgs a)
         if (softmax || a.renorm)
             q = slots_sum(g * p, a.K);
         if (a.renorm) {
-            const float one = __builtin_amdgcn_rcpf(slots_sum(p, a.K) + kTiny);
-            dp = kTiny * g;
+            // (each factor 1 / D at once: g p and 1e-20 g p may be below what f32 holds)
+            const float one = __builtin_amdgcn_rcpf(slots_sum(p, a.K) + kTiny), tiny = kTiny * one, share = p * one;
+            dp = tiny * g;
             for (uint64_t left = slots; left; left &= left - 1) {
                 const int i = __builtin_ctzll(left);
-                dp = __builtin_fmaf(lane_of(p, i), g - lane_of(g, i), dp);
+                dp = __builtin_fmaf(lane_of(share, i), g - lane_of(g, i), dp);
             }
-            dp = dp * one * one;
-            q = kTiny * q * one * one;
+            dp = dp * one;
+            q = tiny * (q * one);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)

@@ -1,0 +1,31 @@
+"""moe_gate_bwd on the GPU at the end of its range: chosen scores whose sum comes near the
+1e-20 that is added to it."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_grouped_gemm_amd as moe
+import layer_util as lu
+from parity_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", list(lu.DT))
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+def test_gradient_of_chosen_scores_next_to_nothing(sigmoid, dtype):
+    # a router with a balance bias may choose experts whose own scores are e^-40 to e^-70
+    say(f"gate gradient of tiny scores {dtype}")
+    T, E, K = 32, 96, 4
+    rng = np.random.default_rng(11)
+    l = torch.from_numpy(rng.standard_normal((T, E)))
+    idx = torch.from_numpy(np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32))
+    far = torch.linspace(38, 70, T).double()[:, None].expand(T, K)
+    l.scatter_(1, idx.long(), -far + 0.5 * torch.from_numpy(rng.standard_normal((T, K))))
+    l = l.to(lu.DT[dtype])
+    dw = torch.from_numpy(rng.standard_normal((T, K))).float()
+    got = moe.moe_gate_bwd(l.cuda(), idx.cuda(), dw.cuda(), score=int(sigmoid), renorm=True)
+    want, mag = lu.gate_grad(lu.f64(l), idx.numpy(), lu.f64(dw), sigmoid, True, 1.0)
+    # as for ordinary scores: the scores' roundings in dp's terms and twice in D, a run over the slots, the score
+    steps = 4 * lu.gate_steps(lu.f64(l), E) + 2 * K + 25
+    lu.within(got, want, lu.rounded_bound(want, steps * lu.U32 * mag, lu.DT[dtype]))
