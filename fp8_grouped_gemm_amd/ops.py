@@ -482,8 +482,9 @@ def moe_gate(logits, top_k, bias=None, mask=None, score=MOE_SCORE_SOFTMAX, group
     dev = logits.get_device()
     dt, T, E = _matrix(logits, "logits", _DTYPES)
     _int32("sizes", max(map(abs, (top_k, score, groups, top_groups, group_top))))
+    if top_k > E:  # (before outputs of that size)
+        _check(MOE_ERR_INVALID_ARG, "moe_gate")
     slots = (T, max(top_k, 0))
-    _int32("topk_idx", slots[0] * slots[1])
     if mask is not None and mask.dtype is torch.bool:
         mask = mask.view(torch.uint8)
     given = tuple(t for t in (topk_idx, topk_w) if t is not None)
@@ -509,7 +510,7 @@ def moe_gate_bwd(logits, topk_idx, dw, score=MOE_SCORE_SOFTMAX, renorm=True, sca
     if topk_idx.dim() != 2:
         raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [T, K]")
     K = topk_idx.shape[1]
-    _int32("topk_idx", max(T * K, abs(score)))
+    _int32("sizes", max(K, abs(score)))
     if dw.requires_grad and torch.is_grad_enabled():
         _lost("dw")
     given = out

@@ -1,5 +1,5 @@
-"""moe_gate_bwd on the GPU at the end of its range: chosen scores whose sum comes near the
-1e-20 that is added to it."""
+"""moe_gate and moe_gate_bwd on the GPU at the ends of their ranges: chosen scores whose sum
+comes near the 1e-20 that is added to it, and more slots than 31 bits count."""
 import numpy as np
 import pytest
 import torch
@@ -29,3 +29,26 @@ def test_gradient_of_chosen_scores_next_to_nothing(sigmoid, dtype):
     # as for ordinary scores: the scores' roundings in dp's terms and twice in D, a run over the slots, the score
     steps = 4 * lu.gate_steps(lu.f64(l), E) + 2 * K + 25
     lu.within(got, want, lu.rounded_bound(want, steps * lu.U32 * mag, lu.DT[dtype]))
+
+
+def test_more_slots_than_31_bits():
+    say("gate: 2^31 slots and more")
+    T, E, K, n = (1 << 27) + 77, 16, 16, 300
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    l[-n:].normal_()
+    idx, w = moe.moe_gate(l, K)
+    a, b = moe.moe_gate(l[-n:].clone(), K)
+    assert torch.equal(idx[-n:], a) and torch.equal(w[-n:], b)
+    assert torch.equal(idx[:n], torch.arange(K, device="cuda", dtype=torch.int32).expand(n, K))
+    w[:-n] = 1.0
+    w[-n:].normal_()
+    d = moe.moe_gate_bwd(l, idx, w, renorm=False)
+    assert torch.equal(d[-n:], moe.moe_gate_bwd(l[-n:].clone(), a, w[-n:].clone(), renorm=False))
+    del l, d, idx, w
+    torch.cuda.empty_cache()
+
+
+def test_more_slots_than_experts_are_refused_before_they_are_allocated():
+    l = torch.zeros(1 << 20, 32, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.moe_gate(l, 1 << 30)                              # (2^52 bytes)
