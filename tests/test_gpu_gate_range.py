@@ -31,6 +31,23 @@ def test_gradient_of_chosen_scores_next_to_nothing(sigmoid, dtype):
     lu.within(got, want, lu.rounded_bound(want, steps * lu.U32 * mag, lu.DT[dtype]))
 
 
+def test_gradient_of_experts_far_below_the_best():
+    # logits whose differences are exact, so that no rounding grows with them; beside the best expert the others'
+    # terms are too small to count in the sum.  Roundings: exp 4 (2 the hardware's, 2 of its argument's repair), the sum's 3
+    # levels of lanes and 3 of rows, its reciprocal 2, their product; the same but for exp, which is 1, of the best
+    # expert's score; times dw, and the product
+    say("gate gradient of far experts")
+    T, E = 500, 64
+    g = torch.Generator().manual_seed(2)
+    l = -(20 + torch.randint(0, 60 * 64, (T, E), generator=g) / 64.0)
+    l[:, 0] = 0
+    dw = torch.rand(T, 1, generator=g) + 0.5
+    idx = torch.zeros(T, 1, dtype=torch.int32)
+    got = moe.moe_gate_bwd(l.cuda(), idx.cuda(), dw.cuda(), renorm=False)
+    want, mag = lu.gate_grad(lu.f64(l), idx.numpy(), lu.f64(dw), False, False, 1.0)
+    lu.within(got[:, 1:], want[:, 1:], (4 + (6 + 2 + 1) + (6 + 2 + 1) + 2) * lu.U32 * mag[:, 1:])
+
+
 def test_more_slots_than_31_bits():
     say("gate: 2^31 slots and more")
     T, E, K, n = (1 << 27) + 77, 16, 16, 300
