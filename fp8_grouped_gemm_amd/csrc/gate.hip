@@ -18,11 +18,12 @@
 // elsewhere the token's c are formed in 64 bits.
 //
 // Instructions bound it: 8192 tokens of 256 experts, sigmoid and bias, 4 of 8 groups, top-8
-// take 11.1 us of which 10 are the call, 32768 tokens 30.3, where the logits take 7 to read.  The
-// gradient moves 52 MB of 32768 x 384 bf16 in 13.5 us, 3.7 TB/s; waves that walk the tokens and
-// load the next one early take 16.0.  Runs of at most eight experts make most calls; 32768 tokens
-// of 512 experts, 8 groups, top-8: 47 - 49 us, of 1024 with runs of 16 92, of 1000 in 10 groups with
-// runs of 25 (in instances for 32) 410 - 455: a run's sort grows with its square.
+// take 11.1 us of which 10 are the call, 32768 tokens 30.3 (27.8 if the kernel had no 64-bit part, which one
+// token in a thousand needs), where the logits take 7 to read.  The gradient moves 52 MB of
+// 32768 x 384 bf16 in 13.5 us, 3.7 TB/s; waves that walk the tokens and load the next one
+// early take 16.0.  Runs of at most eight experts make most calls; 32768 tokens of 512 experts,
+// 8 groups, top-8: 47 - 50 us, of 1024 with runs of 16 92, of 1000 in 10 groups with runs of 25 (in
+// instances for 32) 410 - 480: a run's sort grows with its square.
 #include "../../include/moe_ops.h"
 #include "ops_internal.h"
 #include "rows_device.h"
@@ -203,6 +204,8 @@ __device__ __forceinline__ float softmax_sum(const float* l, float& m, float* e)
     return wave_sum(z);
 }
 
+// The hardware's reciprocal, here and below: a Newton step behind each left the weights of 2^18 tokens
+// as they are (softmax, renormalised) or a little further off (mean 0.61 roundings for 0.54, sigmoid).
 __device__ __forceinline__ float sigmoid(float l) { return __builtin_amdgcn_rcpf(1.f + expf(-l)); }
 
 // Whether two f32 values of c, above >= below, are too near for their order to be sure; in

@@ -278,9 +278,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wgrad_tile(Wgra
 
     // Workgroups go to the 8 dies in turn.  Of every unit's (a share of an expert's) tiles, counted
     // down strips of kStrip rows, a die takes a run: a compact block, whose rows and
-    // columns its L2 holds (32 experts of 384 rows, 4096 x 4096: 568 us with strips of 4
-    // tiles, 584 of 8, 596 of 16); the die that gets the last, shorter run changes from unit
-    // to unit.  Shares of one expert are equally long, so that the dies take runs of them all.
+    // columns its L2 holds (strips of 2, 4, 8 and 16 tiles: 32 experts of 384 rows, 4096 x 4096 567,
+    // 564, 585 and 591 us; 8192^3 921, 918, 927 and 933; seven other sizes within 7 %, of 2 and 4
+    // within 5); the die that gets the last, shorter run changes from unit to unit.  Shares
+    // of one expert are equally long, so that the dies take runs of them all.
     const unsigned tiles = tiles_m * tiles_n, die = workgroup() & 7, turn = workgroup() >> 3;
     unsigned unit, tile;
     if (a.E == 1) {
@@ -504,8 +505,10 @@ namespace {
 
 // The kernels: a tile's rows and columns, workgroups that run at a time, and in us a stage of
 // 64 rows with one workgroup on the card and with all of them, and a tile's start and results.
-// Fitted to a sweep of all three with 1 to 16 shares over 27 sizes; the choice is within 5 % of
-// the best.  us of the three, each with its best number of shares (bf16, UE8M0, to f32):
+// Fitted to a sweep of all three with 1 to 16 shares over 27 sizes, experts equally long: the
+// kernel that is chosen, forced as the others are, is within 5 % of the best (called by itself,
+// first in each row of the sweep, it took up to 8 % more than the best).  us of the three, each with
+// its best number of shares (bf16, UE8M0, to f32):
 //   groups x rows in all, n x k   128 x 128    128 x 256    256 x 256
 //   1 x 128, 512 x 512             8.6          8.5          9.7
 //   1 x 512, 1024 x 1024          10.1         12.5         18.1
